@@ -30,6 +30,13 @@
  * section "Where llama.cpp is still ahead", K-quant item): they are never
  * quantized.
  *
+ *   MXFP4 32 weights sharing one power of two: e2m1 codes (sign, two exponent
+ *         bits, one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and a scale byte s;
+ *         w = e2m1 * 2^(s-127), s = 255 is NaN for the whole block.  Held as two
+ *         planes instead of interleaved blocks: codes [rows][K/2], the even column
+ *         in the low nibble, and scales [rows][K/32] (the blocks then start
+ *         aligned and are the matrix instructions' operands as they lie).
+ *
  * Conventions for every entry point:
  *   - All buffer pointers are device pointers on the current HIP device,
  *     allocated and owned by the caller; the library never allocates, frees
@@ -67,6 +74,13 @@ typedef enum gq_status {
     GQ_EWORKSPACE = 4, /* workspace missing or smaller than gq_moe_workspace_bytes() */
     GQ_EHIP = 5        /* the HIP runtime reported an error at launch */
 } gq_status;
+
+/* Element types of the entry points that take more than one. */
+typedef enum gq_dtype {
+    GQ_F32 = 0, /* binary32 */
+    GQ_F16 = 1, /* binary16 */
+    GQ_BF16 = 2 /* bfloat16 */
+} gq_dtype;
 
 /* Largest batch accepted by the matrix-vector products. */
 #define GQ_GEMV_MAX_BATCH 16
@@ -438,6 +452,75 @@ gq_status gq_dequant_q8_0(const void *w, float *out32, uint16_t *out16, int64_t 
                           void *stream);
 gq_status gq_dequant_q4k(const void *w, float *out32, uint16_t *out16, int64_t M, int64_t K,
                          void *stream);
+
+/* Microscaled 4-bit (MXFP4) operators: the same forms of the fused product over
+ * MXFP4 weights (the planes described above; this library's own addition, the
+ * pages name no such format).  An MXFP4 weight is exact in binary32 and in
+ * bfloat16 for s <= 252 (above, values of 2^128 and more are infinities); in binary16 it is exact for scales 104 <= s <= 140, else rounded once
+ * (nearest even, overflow to infinity), as the other formats' weights are.  A
+ * block with s = 255 makes every product it enters NaN; so do infinities in the
+ * activations, except where the sums of the definition are infinite (either may
+ * come back).
+ *
+ * gq_quantize_mxfp4: per block of 32 values of a row,
+ *   s = clamp(floor(log2(max|x|)) - 2, -127, 127) + 127,
+ *   code = x * 2^(127-s) rounded to the nearest e2m1 value (ties to the even
+ *          code), magnitudes above 6 to 6; zero keeps its sign.
+ * An all-zero block has s = 0; a block holding an infinity or a NaN has s = 255
+ * and zero codes.  x: N rows of K elements of x_type (any gq_dtype), ldx elements
+ * apart, ldx >= K, every row 16-byte aligned (ldx unused when N is 1).
+ * q: [N][K/2], s: [N][K/32].  Requires K % 32 == 0, N*K <= 2^34; q and s must not
+ * overlap x. */
+gq_status gq_quantize_mxfp4(const void *x, int x_type, int64_t ldx, uint8_t *q, uint8_t *s,
+                            int64_t N, int64_t K, void *stream);
+
+/* The values of an MXFP4 matrix: out [M][K] of out_type (any gq_dtype), rounded
+ * as said above.  Requires K % 32 == 0, M*K <= 2^34. */
+gq_status gq_dequant_mxfp4(const uint8_t *q, const uint8_t *s, void *out, int out_type, int64_t M,
+                           int64_t K, void *stream);
+
+/* MXFP4 matrix-vector product, binary32 activations, 1 <= B <= GQ_GEMV_MAX_BATCH:
+ *   y[b][r] = sum_k w[r][k] * x[b][k], products exact, sums binary32
+ * (GQ_GEMV_ACCURACY; magnitudes of x or of products below 2^-126 may be lost).
+ * wq: [M][K/2], ws: [M][K/32], x: [B][K], y: [B][M].  Requires K % 32 == 0,
+ * M <= 2^26. */
+gq_status gq_gemv_mxfp4(const uint8_t *wq, const uint8_t *ws, const float *x, float *y, int64_t M,
+                        int64_t K, int64_t B, void *stream);
+
+/* MXFP4 matrix product, activations and output of one 16-bit type (GQ_F16 or
+ * GQ_BF16), any number of activation rows:
+ *   Y[n][r] = round( sum_k X[n][k] * w[r][k] ), sums binary32, one rounding,
+ * w as rounded to that type (bfloat16: exact).  x: [N][K], y: [N][M].  Requires
+ * K % 32 == 0, M <= 2^26, N <= 2^21. */
+gq_status gq_gemm_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint16_t *x, uint16_t *y,
+                        int type, int64_t M, int64_t K, int64_t N, void *stream);
+
+/* The product of two MXFP4 matrices on the scaled 4-bit matrix cores, xq/xs from
+ * gq_quantize_mxfp4 (opt-in, as the integer-dot path is: results move from the
+ * unquantized product by the quantisation of x):
+ *   Y[n][r] = round( sum_k v(xq, xs)[n][k] * w[r][k] ), sums binary32,
+ * Y [N][M] of y_type (any gq_dtype).  Requires K % 32 == 0, M <= 2^26,
+ * N <= 2^21. */
+gq_status gq_gemm_mxfp4_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint8_t *xq,
+                              const uint8_t *xs, void *y, int y_type, int64_t M, int64_t K,
+                              int64_t N, void *stream);
+
+/* The mixture-of-experts feed-forward over MXFP4 expert stacks: the formula of
+ * gq_moe_gemm_q4k (input_weighted != 0: of gq_moe_gemm_q4k_input_weighted) with
+ * x, h and out of `type` (GQ_F16 or GQ_BF16) and weights as in gq_gemm_mxfp4.
+ * wq_gate, wq_up: [E][I][H/2], ws_gate, ws_up: [E][I][H/32]; wq_down: [E][H][I/2],
+ * ws_down: [E][H][I/32].  ws: at least gq_moe_mxfp4_workspace_bytes() bytes,
+ * regions as in gq_moe_workspace_offsets; contents on entry are ignored; not to be
+ * in use by another call while this one runs.  Requires H % 32 == 0,
+ * I % 32 == 0, H, I <= 2^26, 1 <= topk <= E <= 256, T*topk <= 2^20, T*H <= 2^34.
+ * Slots with an id outside [0, E) are skipped. */
+gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, const uint8_t *wq_up,
+                            const uint8_t *ws_up, const uint8_t *wq_down, const uint8_t *ws_down,
+                            const uint16_t *x, const int32_t *topk_ids, const float *topk_w,
+                            uint16_t *out, int type, int64_t T, int64_t H, int64_t I, int64_t E,
+                            int64_t topk, int64_t input_weighted, void *ws, size_t ws_bytes,
+                            void *stream);
+size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
 
 /* Diagnostics. */
 const char *gq_last_error(void);       /* message of this thread's last failed call */

@@ -9,74 +9,15 @@
 #include "gq.h"
 
 #include <hip/hip_runtime.h>
-#include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
+#include "gq_checks.h"
 #include "gq_internal.h"
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-gq_status fail(gq_status s, const char *fmt, ...)
-{
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-gq_status check_ptr(const char *fn, const char *name, const void *p)
-{
-    if (!p)
-        return fail(GQ_EINVAL, "%s: %s is NULL", fn, name);
-    if (!aligned16(p))
-        return fail(GQ_EALIGN, "%s: %s (%p) is not 16-byte aligned", fn, name, p);
-    return GQ_OK;
-}
-
-// Sizes the kernels index with 32-bit row/column counts.
-constexpr int64_t kMaxDim = (int64_t)1 << 30;
-
-gq_status check_dim(const char *fn, const char *name, int64_t v, bool allow_zero)
-{
-    if (v < 0 || (!allow_zero && v == 0))
-        return fail(GQ_EINVAL, "%s: %s = %lld must be %s", fn, name, (long long)v,
-                    allow_zero ? "non-negative" : "positive");
-    if (v > kMaxDim)
-        return fail(GQ_ESHAPE, "%s: %s = %lld exceeds the supported maximum %lld", fn, name,
-                    (long long)v, (long long)kMaxDim);
-    return GQ_OK;
-}
-
-gq_status check_k(const char *fn, const char *name, int64_t K, int64_t block)
-{
-    gq_status st = check_dim(fn, name, K, false);
-    if (st != GQ_OK)
-        return st;
-    if (K % block != 0)
-        return fail(GQ_ESHAPE, "%s: %s = %lld is not a multiple of the %lld-weight block", fn,
-                    name, (long long)K, (long long)block);
-    return GQ_OK;
-}
-
-gq_status launched(const char *fn, hipError_t e)
-{
-    if (e != hipSuccess)
-        return fail(GQ_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
-    return GQ_OK;
-}
-
-#define GQ_TRY(expr)                                                                           \
-    do {                                                                                       \
-        gq_status st_ = (expr);                                                                \
-        if (st_ != GQ_OK)                                                                      \
-            return st_;                                                                        \
-    } while (0)
+using namespace gq::checks;
 
 gq_status gemv_checks(const char *fn, const void *w, const float *x, float *y, int64_t M,
                       int64_t K, int64_t B, int64_t block)
@@ -91,42 +32,6 @@ gq_status gemv_checks(const char *fn, const void *w, const float *x, float *y, i
     GQ_TRY(check_ptr(fn, "w", w));
     GQ_TRY(check_ptr(fn, "x", x));
     GQ_TRY(check_ptr(fn, "y", y));
-    return GQ_OK;
-}
-
-constexpr size_t kAlign = 256;
-size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-gq_status moe_layout(const char *fn, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
-                     size_t off[7])
-{
-    GQ_TRY(check_dim(fn, "T", T, true));
-    GQ_TRY(check_k(fn, "H", H, 256));
-    GQ_TRY(check_k(fn, "I", I, 256));
-    if (E < 1 || E > 256)
-        return fail(GQ_ESHAPE, "%s: E = %lld is outside the supported range [1, 256]", fn,
-                    (long long)E);
-    if (topk < 1 || topk > E)
-        return fail(GQ_EINVAL, "%s: topk = %lld is outside [1, E = %lld]", fn, (long long)topk,
-                    (long long)E);
-    const int64_t A = T * topk;
-    if (A > ((int64_t)1 << 20))
-        return fail(GQ_ESHAPE, "%s: T*topk = %lld exceeds the supported maximum %lld", fn,
-                    (long long)A, (long long)1 << 20);
-    size_t o = 0;
-    off[0] = o;
-    o = up(o + (size_t)(E + 3) * 4);
-    off[1] = o;
-    o = up(o + (size_t)A * 4);
-    off[2] = o;
-    o = up(o + (size_t)A * 4);
-    off[3] = o;
-    o = up(o + (size_t)2 * (A + E) * 4);
-    off[4] = o;
-    o = up(o + (size_t)A * I * 2);
-    off[5] = o;
-    o = up(o + (size_t)A * H * 4);
-    off[6] = o;
     return GQ_OK;
 }
 
@@ -567,7 +472,7 @@ size_t gq_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_
     size_t off[7];
     char saved[sizeof g_err];
     memcpy(saved, g_err, sizeof g_err);
-    const gq_status st = moe_layout("gq_moe_workspace_bytes", T, H, I, E, topk, off);
+    const gq_status st = moe_layout("gq_moe_workspace_bytes", T, H, I, E, topk, 256, off);
     if (st != GQ_OK)
         return 0;
     memcpy(g_err, saved, sizeof g_err);
@@ -579,7 +484,7 @@ gq_status gq_moe_workspace_offsets(int64_t T, int64_t H, int64_t I, int64_t E, i
 {
     if (!off)
         return fail(GQ_EINVAL, "gq_moe_workspace_offsets: off is NULL");
-    return moe_layout("gq_moe_workspace_offsets", T, H, I, E, topk, off);
+    return moe_layout("gq_moe_workspace_offsets", T, H, I, E, topk, 256, off);
 }
 
 static gq_status moe_common(const char *fn, const void *w_gate, const void *w_up,
@@ -591,7 +496,7 @@ static gq_status moe_common(const char *fn, const void *w_gate, const void *w_up
     gq::MoeArgs a;
     a.weight_input = weight_input;
     a.q8_0 = q8_0;
-    GQ_TRY(moe_layout(fn, T, H, I, E, topk, a.off));
+    GQ_TRY(moe_layout(fn, T, H, I, E, topk, 256, a.off));
     if (T == 0)
         return GQ_OK;
     GQ_TRY(check_ptr(fn, "w_gate", w_gate));

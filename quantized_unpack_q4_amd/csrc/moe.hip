@@ -17,6 +17,7 @@
 // No atomics touch the outputs and nothing waits on the host.
 #include "gq_device.h"
 #include "gq_internal.h"
+#include "mxfp4_device.h"
 
 namespace gq {
 
@@ -205,7 +206,9 @@ __global__ __launch_bounds__(kGroupThreads) void moe_group_kernel(
     }
 }
 
-// One thread per 4 output columns of one token.
+// One thread per 4 output columns of one token; BF16: a bfloat16 output instead
+// of binary16.
+template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restrict__ D,
                                                           const int32_t *__restrict__ pos_of,
                                                           const float *__restrict__ wts,
@@ -229,7 +232,33 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restric
         a3 = fmaf(wgt, d.w, a3);
     }
     *reinterpret_cast<uint2 *>(out + (int64_t)t * H + c) =
-        make_uint2(pack_half2(a0, a1), pack_half2(a2, a3));
+        make_uint2(mx_pack2<BF16>(a0, a1), mx_pack2<BF16>(a2, a3));
+}
+
+hipError_t launch_moe_group(const int32_t *ids, uint8_t *ws, const size_t *off, int64_t A,
+                            int64_t E, int bn, int max_tiles, hipStream_t s)
+{
+    hipLaunchKernelGGL(moe_group_kernel, dim3(1), dim3(kGroupThreads), 0, s, ids, (int)A, (int)E,
+                       bn, max_tiles, reinterpret_cast<int32_t *>(ws + off[0]),
+                       reinterpret_cast<int32_t *>(ws + off[1]),
+                       reinterpret_cast<int32_t *>(ws + off[2]),
+                       reinterpret_cast<int32_t *>(ws + off[3]));
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const float *d, const int32_t *pos_of, const float *wts,
+                              uint16_t *out, bool bf16, int64_t T, int64_t H, int64_t topk,
+                              bool unit, hipStream_t s)
+{
+    const int col_blocks = (int)((H / 4 + 255) / 256);
+    const dim3 grid((unsigned)(T * col_blocks));
+    if (bf16)
+        hipLaunchKernelGGL((moe_combine_kernel<true>), grid, dim3(256), 0, s, d, pos_of, wts, out,
+                           (int)H, (int)topk, col_blocks, (int)unit);
+    else
+        hipLaunchKernelGGL((moe_combine_kernel<false>), grid, dim3(256), 0, s, d, pos_of, wts, out,
+                           (int)H, (int)topk, col_blocks, (int)unit);
+    return hipGetLastError();
 }
 
 hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
@@ -240,13 +269,7 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     const bool big = moe_big_applies(A, a.E, a.H, a.I) && (!a.q8_0 || a.I % 256 == 0);
     const int bn = big ? moe_big_token_tile() : moe_token_tile(A, a.E);
     const int max_tiles = (int)((A + bn - 1) / bn + a.E);
-    int32_t *offsets = reinterpret_cast<int32_t *>(a.ws + a.off[0]);
-    int32_t *sorted = reinterpret_cast<int32_t *>(a.ws + a.off[1]);
-    int32_t *pos_of = reinterpret_cast<int32_t *>(a.ws + a.off[2]);
-    int32_t *tiles = reinterpret_cast<int32_t *>(a.ws + a.off[3]);
-    hipLaunchKernelGGL(moe_group_kernel, dim3(1), dim3(kGroupThreads), 0, s, a.ids, (int)A,
-                       (int)a.E, bn, max_tiles, offsets, sorted, pos_of, tiles);
-    hipError_t err = hipGetLastError();
+    hipError_t err = launch_moe_group(a.ids, a.ws, a.off, A, a.E, bn, max_tiles, s);
     if (err != hipSuccess)
         return err;
     err = big ? launch_moe_big(a, max_tiles, s)
@@ -254,11 +277,9 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
                                            : launch_moe_gemms(a, bn, max_tiles, s);
     if (err != hipSuccess)
         return err;
-    const int col_blocks = (int)((a.H / 4 + 255) / 256);
-    hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)(a.T * col_blocks)), dim3(256), 0, s,
-                       reinterpret_cast<const float *>(a.ws + a.off[5]), pos_of, a.wts, a.out,
-                       (int)a.H, (int)a.topk, col_blocks, a.weight_input);
-    return hipGetLastError();
+    return launch_moe_combine(reinterpret_cast<const float *>(a.ws + a.off[5]),
+                              reinterpret_cast<const int32_t *>(a.ws + a.off[2]), a.wts, a.out,
+                              false, a.T, a.H, a.topk, a.weight_input != 0, s);
 }
 
 } // namespace gq

@@ -21,6 +21,9 @@ GQ_EALIGN = 3
 GQ_EWORKSPACE = 4
 GQ_EHIP = 5
 MAX_BATCH = 16
+GQ_F32 = 0
+GQ_F16 = 1
+GQ_BF16 = 2
 
 EXPORTS = (
     "gq_gemv_q8_0", "gq_gemv_q4k", "gq_gemv_q4k_multi_table_bytes", "gq_gemv_q4k_multi_plan",
@@ -32,7 +35,8 @@ EXPORTS = (
     "gq_moe_gemm_q8_0_input_weighted", "gq_moe_route", "gq_quantize_q8k", "gq_gemv_q4k_q8k",
     "gq_gemm_q4k_q8k",
     "gq_moe_workspace_bytes", "gq_moe_workspace_offsets", "gq_dequant_q8_0",
-    "gq_dequant_q4k", "gq_last_error", "gq_status_str", "gq_version",
+    "gq_dequant_q4k", "gq_quantize_mxfp4", "gq_dequant_mxfp4", "gq_gemv_mxfp4", "gq_gemm_mxfp4",
+    "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes", "gq_last_error", "gq_status_str", "gq_version",
 )
 
 
@@ -115,6 +119,21 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = st
             f.argtypes = [vp, vp, vp, i64, i64, vp]
+        ci = ctypes.c_int
+        L.gq_quantize_mxfp4.restype = st
+        L.gq_quantize_mxfp4.argtypes = [vp, ci, i64, vp, vp, i64, i64, vp]
+        L.gq_dequant_mxfp4.restype = st
+        L.gq_dequant_mxfp4.argtypes = [vp, vp, vp, ci, i64, i64, vp]
+        L.gq_gemv_mxfp4.restype = st
+        L.gq_gemv_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        L.gq_gemm_mxfp4.restype = st
+        L.gq_gemm_mxfp4.argtypes = [vp, vp, vp, vp, ci, i64, i64, i64, vp]
+        L.gq_gemm_mxfp4_mxfp4.restype = st
+        L.gq_gemm_mxfp4_mxfp4.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp]
+        L.gq_moe_gemm_mxfp4.restype = st
+        L.gq_moe_gemm_mxfp4.argtypes = [vp] * 10 + [ci] + [i64] * 6 + [vp, sz, vp]
+        L.gq_moe_mxfp4_workspace_bytes.restype = sz
+        L.gq_moe_mxfp4_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
         L.gq_last_error.restype = ctypes.c_char_p
         L.gq_last_error.argtypes = []
         L.gq_status_str.restype = ctypes.c_char_p
@@ -341,6 +360,44 @@ def gq_dequant_q4k(w, out32, out16, M, K, stream=None):
     _check(lib().gq_dequant_q4k(_ptr(w), _ptr(out32), _ptr(out16), M, K, _stream(stream)))
 
 
+def gq_quantize_mxfp4(x, x_type, ldx, q, s, N, K, stream=None):
+    """x may be a strided view: rows ldx elements apart."""
+    _check(lib().gq_quantize_mxfp4(ctypes.c_void_p(x.data_ptr()), x_type, ldx, _ptr(q), _ptr(s),
+                                   N, K, _stream(stream)))
+
+
+def gq_dequant_mxfp4(q, s, out, out_type, M, K, stream=None):
+    _check(lib().gq_dequant_mxfp4(_ptr(q), _ptr(s), _ptr(out), out_type, M, K, _stream(stream)))
+
+
+def gq_gemv_mxfp4(wq, ws, x, y, M, K, B, stream=None):
+    _check(lib().gq_gemv_mxfp4(_ptr(wq), _ptr(ws), _ptr(x), _ptr(y), M, K, B, _stream(stream)))
+
+
+def gq_gemm_mxfp4(wq, ws, x, y, dtype, M, K, N, stream=None):
+    _check(lib().gq_gemm_mxfp4(_ptr(wq), _ptr(ws), _ptr(x), _ptr(y), dtype, M, K, N,
+                               _stream(stream)))
+
+
+def gq_gemm_mxfp4_mxfp4(wq, ws, xq, xs, y, y_type, M, K, N, stream=None):
+    _check(lib().gq_gemm_mxfp4_mxfp4(_ptr(wq), _ptr(ws), _ptr(xq), _ptr(xs), _ptr(y), y_type, M,
+                                     K, N, _stream(stream)))
+
+
+def gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk) -> int:
+    return int(lib().gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk))
+
+
+def gq_moe_gemm_mxfp4(wq_gate, ws_gate, wq_up, ws_up, wq_down, ws_down, x, topk_ids, topk_w, out,
+                      dtype, T, H, I, E, topk, input_weighted, ws, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gq_moe_gemm_mxfp4(_ptr(wq_gate), _ptr(ws_gate), _ptr(wq_up), _ptr(ws_up),
+                                   _ptr(wq_down), _ptr(ws_down), _ptr(x), _ptr(topk_ids),
+                                   _ptr(topk_w), _ptr(out), dtype, T, H, I, E, topk,
+                                   int(input_weighted), _ptr(ws), ws_bytes, _stream(stream)))
+
+
 def gq_version() -> int:
     return int(lib().gq_version())
 
@@ -438,3 +495,148 @@ def quantize_q8k(x, stream=None):
     bs = torch.empty((B, K // 32), dtype=torch.int32, device=x.device)
     gq_quantize_q8k(x, q, d, bs, B, K, stream)
     return q, d, bs
+
+
+# -- microscaled 4-bit (MXFP4): codes uint8 [..][K/2], scales uint8 [..][K/32] -----
+
+def _mx_dtype(dtype, f32=True) -> int:
+    import torch
+    code = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}.get(dtype)
+    if code is None or (code == GQ_F32 and not f32):
+        raise ValueError("unsupported dtype %s" % dtype)
+    return code
+
+
+def _mx_check(name, t, dtype=None, shape=None):
+    """A device tensor of this dtype and shape, on the current device."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, not on the current device" % (name, t.device))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s is %s, expected %s" % (name, t.dtype, dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return t
+
+
+def _mx_planes(name, q, s):
+    """The logical shape (.., rows, K) of an MXFP4 matrix or stack."""
+    import torch
+    _mx_check(name + " codes", q, torch.uint8)
+    K = q.shape[-1] * 2
+    _mx_check(name + " scales", s, torch.uint8, tuple(q.shape[:-1]) + (K // 32,))
+    return tuple(q.shape[:-1]) + (K,)
+
+
+def _mx_out(out, shape, dtype, device, stream):
+    """The output: `out` checked, or a new tensor that belongs to the stream of the call."""
+    import torch
+    if out is not None:
+        return _mx_check("out", out, dtype, shape)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def quantize_mxfp4(x, stream=None):
+    """x [..][K] (float32, float16 or bfloat16; the last dimension contiguous, a
+    two-dimensional x may have strided rows) -> (codes uint8 [..][K/2], scales
+    uint8 [..][K/32])."""
+    import torch
+    code = _mx_dtype(x.dtype)
+    _mx_check("x", x)
+    K = x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    if x.dim() == 2 and x.stride(-1) == 1:
+        x2 = x
+    else:
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
+        x2 = x.reshape(-1, K) if x.numel() else x.reshape(0, K)
+    N = x2.shape[0]
+    ldx = x2.stride(0) if N > 1 else K
+    q = _mx_out(None, lead + (K // 2,), torch.uint8, x.device, stream)
+    s = _mx_out(None, lead + (K // 32,), torch.uint8, x.device, stream)
+    gq_quantize_mxfp4(x2, code, ldx, q, s, N, K, stream)
+    return q, s
+
+
+def dequant_mxfp4(q, s, dtype=None, out=None, stream=None):
+    """The values of codes [..][K/2] and scales [..][K/32] as float32 (or dtype)."""
+    import torch
+    dtype = torch.float32 if dtype is None else dtype
+    shape = _mx_planes("matrix", q, s)
+    o = _mx_out(out, shape, dtype, q.device, stream)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    gq_dequant_mxfp4(q, s, o, _mx_dtype(dtype), rows, shape[-1], stream)
+    return o
+
+
+def gemv_mxfp4(wq, ws, x, out=None, stream=None):
+    """y [B][M] float32 = x [B][K] float32 * W^T for MXFP4 W [M][K], 1 <= B <= 16."""
+    import torch
+    M, K = _mx_planes("W", wq, ws)
+    _mx_check("x", x, torch.float32)
+    x2 = x.reshape(-1, K)
+    B = x2.shape[0]
+    y = _mx_out(out, (B, M), torch.float32, x.device, stream)
+    gq_gemv_mxfp4(wq, ws, x2, y, M, K, B, stream)
+    return y
+
+
+def gemm_mxfp4(wq, ws, x, out=None, stream=None):
+    """Y [N][M] = X [N][K] * W^T in x's dtype (float16 or bfloat16), MXFP4 W [M][K]."""
+    M, K = _mx_planes("W", wq, ws)
+    code = _mx_dtype(x.dtype, f32=False)
+    _mx_check("x", x)
+    x2 = x.reshape(-1, K)
+    N = x2.shape[0]
+    y = _mx_out(out, (N, M), x.dtype, x.device, stream)
+    gq_gemm_mxfp4(wq, ws, x2, y, code, M, K, N, stream)
+    return y
+
+
+def gemm_mxfp4_mxfp4(wq, ws, xq, xs, dtype=None, out=None, stream=None):
+    """Y [N][M] = X * W^T of two MXFP4 matrices, X [N][K] from quantize_mxfp4; Y is
+    float32 unless dtype (or out) says otherwise."""
+    import torch
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    M, K = _mx_planes("W", wq, ws)
+    N, KX = _mx_planes("X", xq, xs)
+    if KX != K:
+        raise ValueError("X has rows of %d values, W of %d" % (KX, K))
+    y = _mx_out(out, (N, M), dtype, xq.device, stream)
+    gq_gemm_mxfp4_mxfp4(wq, ws, xq, xs, y, _mx_dtype(dtype), M, K, N, stream)
+    return y
+
+
+def moe_mxfp4(w_gate, w_up, w_down, x, topk_ids, topk_w, ws=None, out=None, stream=None,
+              input_weighted=False):
+    """Mixture-of-experts feed-forward over MXFP4 stacks, each a pair (codes, scales):
+    gate and up [E][I][H], down [E][H][I]; x [T][H] float16 or bfloat16.  Returns
+    (out [T][H] in x's dtype, workspace)."""
+    import torch
+    E, I, H = _mx_planes("w_gate", *w_gate)
+    if _mx_planes("w_up", *w_up) != (E, I, H):
+        raise ValueError("w_up differs from w_gate in shape")
+    if _mx_planes("w_down", *w_down) != (E, H, I):
+        raise ValueError("w_down is not [E][H][I]")
+    code = _mx_dtype(x.dtype, f32=False)
+    T, topk = topk_ids.shape
+    _mx_check("x", x, shape=(T, H))
+    _mx_check("topk_ids", topk_ids, torch.int32)
+    _mx_check("topk_w", topk_w, torch.float32, (T, topk))
+    need = gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk)
+    if ws is None:
+        ws = _mx_out(None, (max(need, 16),), torch.uint8, x.device, stream)
+    _mx_check("ws", ws)
+    o = _mx_out(out, (T, H), x.dtype, x.device, stream)
+    gq_moe_gemm_mxfp4(*w_gate, *w_up, *w_down, x, topk_ids, topk_w, o, code, T, H, I, E, topk,
+                      input_weighted, ws, stream=stream)
+    return o, ws
