@@ -491,7 +491,7 @@ gq_status gq_gemv_mxfp4(const uint8_t *wq, const uint8_t *ws, const float *x, fl
  * GQ_BF16), any number of activation rows:
  *   Y[n][r] = round( sum_k X[n][k] * w[r][k] ), sums binary32, one rounding,
  * w as rounded to that type (bfloat16: exact).  x: [N][K], y: [N][M].  Requires
- * K % 32 == 0, M <= 2^26, N <= 2^21. */
+ * K % 32 == 0, M <= 2^26, N <= 2^21, M*N <= 2^37. */
 gq_status gq_gemm_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint16_t *x, uint16_t *y,
                         int type, int64_t M, int64_t K, int64_t N, void *stream);
 
@@ -500,7 +500,7 @@ gq_status gq_gemm_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint16_t *x,
  * unquantized product by the quantisation of x):
  *   Y[n][r] = round( sum_k v(xq, xs)[n][k] * w[r][k] ), sums binary32,
  * Y [N][M] of y_type (any gq_dtype).  Requires K % 32 == 0, M <= 2^26,
- * N <= 2^21. */
+ * N <= 2^21, M*N <= 2^37. */
 gq_status gq_gemm_mxfp4_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint8_t *xq,
                               const uint8_t *xs, void *y, int y_type, int64_t M, int64_t K,
                               int64_t N, void *stream);

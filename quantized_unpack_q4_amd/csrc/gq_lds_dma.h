@@ -20,4 +20,12 @@ __device__ __forceinline__ void load_lds16(const void *gbase, uint32_t voff, uin
                  : "memory", "m0");
 }
 
+// The same for 4 bytes per lane: lane l lands at m0 + 4*l; gbase + voff is a
+// multiple of 4.
+__device__ __forceinline__ void load_lds4(const void *gbase, uint32_t voff, uint32_t m0)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(gbase), "s"(m0)
+                 : "memory", "m0");
+}
+
 } // namespace gq

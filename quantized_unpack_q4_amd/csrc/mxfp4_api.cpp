@@ -12,9 +12,10 @@ namespace {
 
 using namespace gq::checks;
 
-// 256 rows of a launch's first grid dimension are at most 2^32 threads.
+// Largest sizes: a launch has fewer than 2^32 threads in a grid dimension.
 constexpr int64_t kMaxRows = (int64_t)1 << 26;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;
+constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
 constexpr int64_t kMaxValues = (int64_t)1 << 34;
 
 gq_status check_type(const char *fn, const char *name, int type, bool f32)
@@ -48,7 +49,8 @@ gq_status product_checks(const char *fn, int64_t M, int64_t K, int64_t N)
     GQ_TRY(check_most(fn, "M", M, kMaxRows));
     GQ_TRY(check_k(fn, "K", K, 32));
     GQ_TRY(check_dim(fn, "N", N, true));
-    return check_most(fn, "N", N, kMaxTokens);
+    GQ_TRY(check_most(fn, "N", N, kMaxTokens));
+    return check_most(fn, "M*N", M * N, kMaxOutputs);
 }
 
 } // namespace

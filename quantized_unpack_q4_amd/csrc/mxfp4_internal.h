@@ -32,6 +32,15 @@ hipError_t launch_gemm_mxfp4(MxMat w, const uint16_t *x, uint16_t *y, int type, 
 hipError_t launch_gemm_mxfp4_mxfp4(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K,
                                    int64_t N, hipStream_t st);
 
+// Their workgroup-tile forms, for more than a few activation rows (tiles16_fit(K),
+// mx_tiles_fit(K)).
+bool tiles16_fit(int64_t K);
+hipError_t launch_gemm_tiles16(MxMat w, const uint16_t *x, uint16_t *y, int type, int64_t M,
+                               int64_t K, int64_t N, hipStream_t st);
+bool mx_tiles_fit(int64_t K);
+hipError_t launch_mx_tiles(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K, int64_t N,
+                           hipStream_t st);
+
 // The mixture-of-experts layer (workspace regions as in MoeArgs).
 struct MxMoeArgs {
     MxMat gate, up, down; // E stacked matrices each
@@ -45,6 +54,9 @@ struct MxMoeArgs {
     size_t off[7];
     int weight_input;
 };
+// Its expert products on tiles of so many tokens (0: use the weight-streaming kernel).
+int moe_tile16_tokens(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+hipError_t launch_moe_tiles16(const MxMoeArgs &a, int tokens, int max_tiles, hipStream_t st);
 hipError_t launch_moe_mxfp4(const MxMoeArgs &a, hipStream_t st);
 
 // The grouping and combine launches of the mixture-of-experts layer (moe.hip):

@@ -264,6 +264,8 @@ hipError_t launch_gemv_mxfp4(MxMat w, const float *x, float *y, int64_t M, int64
 hipError_t launch_gemm_mxfp4(MxMat w, const uint16_t *x, uint16_t *y, int type, int64_t M,
                              int64_t K, int64_t N, hipStream_t st)
 {
+    if (N > 16 && tiles16_fit(K))
+        return launch_gemm_tiles16(w, x, y, type, M, K, N, st);
     return type == kF16 ? launch_dense<kActF16>(w, x, nullptr, y, type, M, K, N, st)
                         : launch_dense<kActBF16>(w, x, nullptr, y, type, M, K, N, st);
 }
@@ -271,17 +273,14 @@ hipError_t launch_gemm_mxfp4(MxMat w, const uint16_t *x, uint16_t *y, int type, 
 hipError_t launch_gemm_mxfp4_mxfp4(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K,
                                    int64_t N, hipStream_t st)
 {
+    if (N > 16 && mx_tiles_fit(K))
+        return launch_mx_tiles(w, x, y, type, M, K, N, st);
     return launch_dense<kActMx>(w, x.q, x.s, y, type, M, K, N, st);
 }
 
-hipError_t launch_moe_mxfp4(const MxMoeArgs &a, hipStream_t st)
+// Gate/up and down of the experts, weights streamed once per 16 nt tokens.
+static hipError_t launch_moe_skinny16(const MxMoeArgs &a, int nt, int max_tiles, hipStream_t st)
 {
-    const int64_t A = a.T * a.topk, mean = A / a.E;
-    const int nt = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
-    const int bn = 16 * nt, max_tiles = (int)((A + bn - 1) / bn + a.E);
-    hipError_t err = launch_moe_group(a.ids, a.ws, a.off, A, a.E, bn, max_tiles, st);
-    if (err != hipSuccess)
-        return err;
     SkinnyArgs p{};
     p.offsets = reinterpret_cast<const int32_t *>(a.ws + a.off[0]);
     p.sorted = reinterpret_cast<const int32_t *>(a.ws + a.off[1]);
@@ -301,19 +300,31 @@ hipError_t launch_moe_mxfp4(const MxMoeArgs &a, hipStream_t st)
     p.ytype = a.type;
     p.M = (int)a.I;
     p.K = (int)a.H;
-    err = a.type == kF16 ? launch<kActF16, kGateUp>(p, nt, (unsigned)max_tiles, st)
-                         : launch<kActBF16, kGateUp>(p, nt, (unsigned)max_tiles, st);
+    hipError_t err = a.type == kF16 ? launch<kActF16, kGateUp>(p, nt, (unsigned)max_tiles, st)
+                                    : launch<kActBF16, kGateUp>(p, nt, (unsigned)max_tiles, st);
     if (err != hipSuccess)
         return err;
-
     p.w = a.down;
     p.x = a.ws + a.off[4];
     p.y = a.ws + a.off[5];
     p.ytype = kF32;
     p.M = (int)a.H;
     p.K = (int)a.I;
-    err = a.type == kF16 ? launch<kActF16, kDown>(p, nt, (unsigned)max_tiles, st)
-                         : launch<kActBF16, kDown>(p, nt, (unsigned)max_tiles, st);
+    return a.type == kF16 ? launch<kActF16, kDown>(p, nt, (unsigned)max_tiles, st)
+                          : launch<kActBF16, kDown>(p, nt, (unsigned)max_tiles, st);
+}
+
+hipError_t launch_moe_mxfp4(const MxMoeArgs &a, hipStream_t st)
+{
+    const int64_t A = a.T * a.topk;
+    const int tokens = moe_tile16_tokens(a.T, a.H, a.I, a.E, a.topk);
+    // (activations past the tiles' 32-bit offsets: groups of 64 tokens)
+    const int nt = A / a.E < 2 ? 1 : 4, bn = tokens ? tokens : 16 * nt;
+    const int max_tiles = (int)((A + bn - 1) / bn + a.E);
+    hipError_t err = launch_moe_group(a.ids, a.ws, a.off, A, a.E, bn, max_tiles, st);
+    if (err != hipSuccess)
+        return err;
+    err = tokens ? launch_moe_tiles16(a, tokens, max_tiles, st) : launch_moe_skinny16(a, nt, max_tiles, st);
     if (err != hipSuccess)
         return err;
     return launch_moe_combine(reinterpret_cast<const float *>(a.ws + a.off[5]),

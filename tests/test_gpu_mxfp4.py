@@ -202,7 +202,12 @@ def test_gemv_wide_range_activations(B):
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [(16, 32, 1), (1, 64, 5), (40, 96, 16), (130, 2080, 17), (65, 160, 33),
                                    (256, 512, 64), (300, 1056, 65), (257, 4096, 130),
-                                   (128, 14336, 7), (515, 288, 300), (1024, 1024, 512)])
+                                   (128, 14336, 7), (515, 288, 300), (1024, 1024, 512),
+                                   # each tile, each way of reading scales, K runs of one chunk
+                                   (4100, 1024, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
+                                   (14300, 96, 1030), (4096, 4096, 130), (4100, 1152, 130),
+                                   (4100, 2080, 130), (1000, 768, 40), (1000, 800, 40),
+                                   (1000, 1024, 40), (100, 992, 200), (70, 256, 20), (70, 2048, 20)])
 def test_gemm(M, K, N, t):
     q, s, W = weights(10, M, K)
     xd, x64 = as_type(normal(11, N, K), t)
@@ -215,7 +220,10 @@ def test_gemm(M, K, N, t):
 @pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [(16, 32, 1), (1, 64, 5), (40, 96, 16), (130, 2080, 17), (65, 160, 33),
                                    (256, 512, 64), (300, 1056, 65), (257, 4096, 130),
-                                   (128, 14336, 7), (515, 288, 300), (1024, 1024, 512)])
+                                   (128, 14336, 7), (515, 288, 300), (1024, 1024, 512),
+                                   # each tile size, with and without whole 512-column chunks
+                                   (4100, 512, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
+                                   (14300, 96, 1030)])
 def test_mxgemm(M, K, N, t):
     torch = torch_cuda()
     q, s, W = weights(12, M, K)
@@ -377,7 +385,12 @@ def moe_check(st, T, H, I, E, topk, t, iw, ws=None):
 @pytest.mark.parametrize("iw", [False, True])
 @pytest.mark.parametrize("T,H,I,E,topk", [(1, 256, 128, 8, 2), (1, 32, 32, 1, 1), (4, 160, 96, 16, 4),
                                           (33, 288, 224, 4, 3), (70, 256, 256, 2, 1), (150, 512, 96, 4, 2),
-                                          (700, 128, 160, 3, 2)])
+                                          (700, 128, 160, 3, 2),
+                                          # tiles of 32, 128 and 256 tokens, each way of reading
+                                          # scales, remainders of more and fewer than 64 tokens
+                                          (24, 512, 640, 8, 3), (40, 1024, 512, 4, 1),
+                                          (61, 288, 1024, 2, 2), (130, 1024, 512, 4, 2),
+                                          (210, 640, 96, 3, 2), (330, 512, 1056, 2, 1)])
 def test_moe(T, H, I, E, topk, t, iw):
     moe_check(moe_case(20, T, H, I, E, topk, t), T, H, I, E, topk, t, iw)
 

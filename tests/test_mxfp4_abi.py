@@ -77,6 +77,7 @@ def test_gemm_refusals(L):
     refused(L, g(P, P, P, P, P, 7, 8, 64, 2, None), "GQ_EINVAL", "y_type = 7")
     refused(L, g(P, P, P, P, P, F32, 8, 100, 2, None), "GQ_ESHAPE", "K = 100")
     refused(L, g(P, P, P, None, P, F32, 8, 64, 2, None), "GQ_EINVAL", "xs is NULL")
+    refused(L, g(P, P, P, P, P, F32, 1 << 20, 64, 1 << 18, None), "GQ_ESHAPE", "M*N")
     assert g(None, None, None, None, None, F32, 0, 64, 2, None) == 0
 
 
