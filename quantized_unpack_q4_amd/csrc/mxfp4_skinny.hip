@@ -7,25 +7,19 @@
 // the workgroup adds in wave order (a fixed order: results do not vary).
 //
 // In a step a lane takes one whole block (32 weights, 16 bytes, one scale) of
-// weight row lane % 16: block lane / 16 of the step's four.  With 16-bit or
-// binary32 activations it converts the block to 16-bit weights, scale included,
+// weight row lane % 16: block lane / 16 of the step's four.  With 16-bit
+// activations it converts the block to 16-bit weights, scale included,
 // and feeds four 16x16x32 products, whose k order inside the step is permuted
 // alike for both operands (product i takes columns 8i .. 8i+7 of each of the four
 // blocks).  With MXFP4 activations the block and its scale are the operand of one
 // scaled 16x16x128 product.
-//
-// Binary32 activations are split into three bfloat16 parts, x = a + b + c exactly
-// (8 + 8 + 8 significant bits, each part cut toward zero from what is left), and
-// an MXFP4 weight is a bfloat16 number exactly, so the three products are exact
-// and only the binary32 sums round.  Infinite and NaN activations stay in the
-// first part alone.
 #include "mxfp4_device.h"
 
 namespace gq {
 
 namespace {
 
-enum { kActF32 = 0, kActF16 = 1, kActBF16 = 2, kActMx = 3 };
+enum { kActF16 = 1, kActBF16 = 2, kActMx = 3 };
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
 struct SkinnyArgs {
@@ -42,36 +36,6 @@ struct SkinnyArgs {
     const float *wts;
     int weight_input;
 };
-
-// The three bfloat16 parts of eight binary32 values.
-__device__ __forceinline__ void split3(const float (&v)[8], uint4 &a, uint4 &b, uint4 &c)
-{
-    uint32_t pa[4], pb[4], pc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t hi[2], mid[2], lo[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float x = v[2 * i + j];
-            hi[j] = __builtin_bit_cast(uint32_t, x);
-            const float r = x - __builtin_bit_cast(float, hi[j] & 0xffff0000u);
-            mid[j] = __builtin_bit_cast(uint32_t, r);
-            lo[j] = __builtin_bit_cast(uint32_t,
-                                       r - __builtin_bit_cast(float, mid[j] & 0xffff0000u));
-            if ((hi[j] & 0x7f800000u) == 0x7f800000u) {
-                hi[j] |= (hi[j] & 0x7fffffu) ? 0x400000u : 0u; // a NaN stays one when cut
-                mid[j] = lo[j] = 0;
-            }
-        }
-        // upper halves of a pair
-        pa[i] = __builtin_amdgcn_perm(hi[1], hi[0], 0x07060302u);
-        pb[i] = __builtin_amdgcn_perm(mid[1], mid[0], 0x07060302u);
-        pc[i] = __builtin_amdgcn_perm(lo[1], lo[0], 0x07060302u);
-    }
-    a = make_uint4(pa[0], pa[1], pa[2], pa[3]);
-    b = make_uint4(pb[0], pb[1], pb[2], pb[3]);
-    c = make_uint4(pc[0], pc[1], pc[2], pc[3]);
-}
 
 template <int ACT, int MODE, int NT, int NW>
 __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
@@ -165,30 +129,12 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
                 const int64_t xi = xrow[j] * K + 32 * (int64_t)blk;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (ACT == kActF32) {
-                        const float *xp = reinterpret_cast<const float *>(p.x) + xi + 8 * i;
-                        const float4 u0 = ldf4(xp), u1 = ldf4(xp + 4);
-                        float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-                        if (!ok)
+                    uint4 xv = ld16(reinterpret_cast<const uint16_t *>(p.x) + xi + 8 * i);
+                    if (!ok)
+                        xv = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                            for (int z = 0; z < 8; ++z)
-                                v[z] = 0.f;
-                        uint4 xa, xb, xc;
-                        split3(v, xa, xb, xc);
-#pragma unroll
-                        for (int m = 0; m < NMAT; ++m) {
-                            acc[m][j] = mx_mfma16<true>(w[m][i], xa, acc[m][j]);
-                            acc[m][j] = mx_mfma16<true>(w[m][i], xb, acc[m][j]);
-                            acc[m][j] = mx_mfma16<true>(w[m][i], xc, acc[m][j]);
-                        }
-                    } else {
-                        uint4 xv = ld16(reinterpret_cast<const uint16_t *>(p.x) + xi + 8 * i);
-                        if (!ok)
-                            xv = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int m = 0; m < NMAT; ++m)
-                            acc[m][j] = mx_mfma16<BF>(w[m][i], xv, acc[m][j]);
-                    }
+                    for (int m = 0; m < NMAT; ++m)
+                        acc[m][j] = mx_mfma16<BF>(w[m][i], xv, acc[m][j]);
                 }
             }
         }
@@ -254,12 +200,6 @@ hipError_t launch_dense(MxMat w, const void *x, const uint8_t *xs, void *y, int 
 }
 
 } // namespace
-
-hipError_t launch_gemv_mxfp4(MxMat w, const float *x, float *y, int64_t M, int64_t K, int B,
-                             hipStream_t st)
-{
-    return launch_dense<kActF32>(w, x, nullptr, y, kF32, M, K, B, st);
-}
 
 hipError_t launch_gemm_mxfp4(MxMat w, const uint16_t *x, uint16_t *y, int type, int64_t M,
                              int64_t K, int64_t N, hipStream_t st)

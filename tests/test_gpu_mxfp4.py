@@ -166,7 +166,9 @@ def weights(seed, M, K):
 
 
 @pytest.mark.parametrize("B", [1, 2, 3, 4, 5, 6, 7, 8, 11, 15, 16])
-@pytest.mark.parametrize("M,K", [(16, 32), (1, 96), (33, 2080), (100, 4096), (515, 160), (64, 14336)])
+@pytest.mark.parametrize("M,K", [(16, 32), (1, 96), (33, 2080), (100, 4096), (515, 160), (64, 14336),
+                                 # several chunks of x, two and four tiles a workgroup
+                                 (40, 16512), (4112, 1056), (8200, 160), (8209, 2080)])
 def test_gemv(M, K, B):
     q, s, W = weights(5, M, K)
     x = normal(6, B, K).astype(np.float32)
