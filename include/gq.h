@@ -483,7 +483,7 @@ gq_status gq_dequant_mxfp4(const uint8_t *q, const uint8_t *s, void *out, int ou
  *   y[b][r] = sum_k w[r][k] * x[b][k], products exact, sums binary32
  * (GQ_GEMV_ACCURACY; magnitudes of x or of products below 2^-126 may be lost).
  * wq: [M][K/2], ws: [M][K/32], x: [B][K], y: [B][M].  Requires K % 32 == 0,
- * M <= 2^26. */
+ * K <= 2^22, M <= 2^26. */
 gq_status gq_gemv_mxfp4(const uint8_t *wq, const uint8_t *ws, const float *x, float *y, int64_t M,
                         int64_t K, int64_t B, void *stream);
 
@@ -491,7 +491,7 @@ gq_status gq_gemv_mxfp4(const uint8_t *wq, const uint8_t *ws, const float *x, fl
  * GQ_BF16), any number of activation rows:
  *   Y[n][r] = round( sum_k X[n][k] * w[r][k] ), sums binary32, one rounding,
  * w as rounded to that type (bfloat16: exact).  x: [N][K], y: [N][M].  Requires
- * K % 32 == 0, M <= 2^26, N <= 2^21, M*N <= 2^37. */
+ * K % 32 == 0, K <= 2^22, M <= 2^26, N <= 2^21, M*N <= 2^37. */
 gq_status gq_gemm_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint16_t *x, uint16_t *y,
                         int type, int64_t M, int64_t K, int64_t N, void *stream);
 
@@ -499,8 +499,8 @@ gq_status gq_gemm_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint16_t *x,
  * gq_quantize_mxfp4 (opt-in, as the integer-dot path is: results move from the
  * unquantized product by the quantisation of x):
  *   Y[n][r] = round( sum_k v(xq, xs)[n][k] * w[r][k] ), sums binary32,
- * Y [N][M] of y_type (any gq_dtype).  Requires K % 32 == 0, M <= 2^26,
- * N <= 2^21, M*N <= 2^37. */
+ * Y [N][M] of y_type (any gq_dtype).  Requires K % 32 == 0, K <= 2^22,
+ * M <= 2^26, N <= 2^21, M*N <= 2^37. */
 gq_status gq_gemm_mxfp4_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint8_t *xq,
                               const uint8_t *xs, void *y, int y_type, int64_t M, int64_t K,
                               int64_t N, void *stream);
@@ -512,7 +512,7 @@ gq_status gq_gemm_mxfp4_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint8_
  * ws_down: [E][H][I/32].  ws: at least gq_moe_mxfp4_workspace_bytes() bytes,
  * regions as in gq_moe_workspace_offsets; contents on entry are ignored; not to be
  * in use by another call while this one runs.  Requires H % 32 == 0,
- * I % 32 == 0, H, I <= 2^26, 1 <= topk <= E <= 256, T*topk <= 2^20, T*H <= 2^34.
+ * I % 32 == 0, H, I <= 2^22, 1 <= topk <= E <= 256, T*topk <= 2^20, T*H < 2^31.
  * Slots with an id outside [0, E) are skipped. */
 gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, const uint8_t *wq_up,
                             const uint8_t *ws_up, const uint8_t *wq_down, const uint8_t *ws_down,

@@ -12,7 +12,10 @@ namespace {
 
 using namespace gq::checks;
 
-// Largest sizes: a launch has fewer than 2^32 threads in a grid dimension.
+// Largest sizes: a launch has fewer than 2^32 threads in a grid dimension, and the tile
+// kernels reach 256 rows of K 16-bit values (the grouped one: all T rows of x) by 32-bit
+// byte offsets.
+constexpr int64_t kMaxK = (int64_t)1 << 22;
 constexpr int64_t kMaxRows = (int64_t)1 << 26;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;
 constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
@@ -48,6 +51,7 @@ gq_status product_checks(const char *fn, int64_t M, int64_t K, int64_t N)
     GQ_TRY(check_dim(fn, "M", M, true));
     GQ_TRY(check_most(fn, "M", M, kMaxRows));
     GQ_TRY(check_k(fn, "K", K, 32));
+    GQ_TRY(check_most(fn, "K", K, kMaxK));
     GQ_TRY(check_dim(fn, "N", N, true));
     GQ_TRY(check_most(fn, "N", N, kMaxTokens));
     return check_most(fn, "M*N", M * N, kMaxOutputs);
@@ -169,10 +173,9 @@ gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, cons
     gq::MxMoeArgs a{};
     GQ_TRY(check_type(fn, "type", type, false));
     GQ_TRY(moe_layout(fn, T, H, I, E, topk, 32, a.off));
-    GQ_TRY(check_most(fn, "H", H, kMaxRows));
-    GQ_TRY(check_most(fn, "I", I, kMaxRows));
-    if (T > 0)
-        GQ_TRY(check_values(fn, "T*H", T, H));
+    GQ_TRY(check_most(fn, "H", H, kMaxK));
+    GQ_TRY(check_most(fn, "I", I, kMaxK));
+    GQ_TRY(check_most(fn, "T*H", T * H, ((int64_t)1 << 31) - 1));
     if (T == 0)
         return GQ_OK;
     GQ_TRY(check_ptr(fn, "wq_gate", wq_gate));

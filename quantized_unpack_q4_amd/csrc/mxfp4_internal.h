@@ -1,6 +1,7 @@
 // mxfp4_internal.h -- launchers of the microscaled 4-bit (MXFP4) operators.
 // Arguments are already validated by mxfp4_api.cpp (sizes positive, K a
-// multiple of 32, pointers non-null and 16-byte aligned) when these are called.
+// multiple of 32 up to 2^22, which keeps the byte offsets of 256 rows of 16-bit values
+// in 32 bits, pointers non-null and 16-byte aligned) when these are called.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -32,12 +33,9 @@ hipError_t launch_gemm_mxfp4(MxMat w, const uint16_t *x, uint16_t *y, int type, 
 hipError_t launch_gemm_mxfp4_mxfp4(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K,
                                    int64_t N, hipStream_t st);
 
-// Their workgroup-tile forms, for more than a few activation rows (tiles16_fit(K),
-// mx_tiles_fit(K)).
-bool tiles16_fit(int64_t K);
+// Their workgroup-tile forms, for more than 16 activation rows.
 hipError_t launch_gemm_tiles16(MxMat w, const uint16_t *x, uint16_t *y, int type, int64_t M,
                                int64_t K, int64_t N, hipStream_t st);
-bool mx_tiles_fit(int64_t K);
 hipError_t launch_mx_tiles(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K, int64_t N,
                            hipStream_t st);
 
@@ -55,13 +53,12 @@ struct MxMoeArgs {
     int weight_input;
 };
 // Its expert products on tiles of so many tokens (0: use the weight-streaming kernel).
-int moe_tile16_tokens(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+int moe_tile16_tokens(int64_t T, int64_t E, int64_t topk);
 hipError_t launch_moe_tiles16(const MxMoeArgs &a, int tokens, int max_tiles, hipStream_t st);
 hipError_t launch_moe_mxfp4(const MxMoeArgs &a, hipStream_t st);
 
 // The grouping and combine launches of the mixture-of-experts layer (moe.hip):
 // token tiles of bn sorted positions.
-struct MoeArgs;
 hipError_t launch_moe_group(const int32_t *ids, uint8_t *ws, const size_t *off, int64_t A,
                             int64_t E, int bn, int max_tiles, hipStream_t st);
 hipError_t launch_moe_combine(const float *d, const int32_t *pos_of, const float *wts,

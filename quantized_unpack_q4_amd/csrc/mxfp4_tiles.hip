@@ -320,11 +320,6 @@ static int mx_tile_choice(int64_t M, int64_t N)
     return t64 <= t128 && t64 <= t256 ? 64 : t128 <= t256 ? 128 : 256;
 }
 
-bool mx_tiles_fit(int64_t K)
-{
-    return K <= (1 << 24); // 32-bit offsets of 256 rows
-}
-
 hipError_t launch_mx_tiles(MxMat w, MxMat x, void *y, int type, int64_t M, int64_t K, int64_t N,
                            hipStream_t st)
 {

@@ -578,11 +578,6 @@ hipError_t launch_dense_choice(const Tile16Args &p, hipStream_t st)
 
 } // namespace
 
-bool tiles16_fit(int64_t K)
-{
-    return K <= (1 << 22); // 32-bit byte offsets of 256 activation rows
-}
-
 hipError_t launch_gemm_tiles16(MxMat w, const uint16_t *x, uint16_t *y, int type, int64_t M,
                                int64_t K, int64_t N, hipStream_t st)
 {
@@ -597,27 +592,24 @@ hipError_t launch_gemm_tiles16(MxMat w, const uint16_t *x, uint16_t *y, int type
 }
 
 // Tokens of a tile of the expert products (0: the weight-streaming kernel), by the mean
-// number of tokens an expert has.  Measured, the whole layer at 64 experts, top-8, hidden
-// 2048, intermediate 1024, binary16: 4 tokens (mean 0.5) 45 us on the weight-streaming
-// kernel, 46 on 32-token tiles, 32 tokens 83 and 75, 128 tokens (mean 16) 138 and 77; 256
-// tokens 88 on 32-token tiles, 83 on 128-token tiles; 1024 tokens (mean 128) 190 on
-// 128-token tiles, 216 on 256-token tiles, 2048 tokens 312 and 284.
-int moe_tile16_tokens(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk)
+// number of tokens an expert has.  Measured, us for the whole layer at 64 experts, top-8,
+// hidden 2048, intermediate 1024, binary16, weights from HBM: 64 tokens (mean 8) 75 on the
+// weight-streaming kernel, 91 on 64-token tiles; 128 tokens 101 and 90; 256 tokens 158, 95
+// and 102 on 128-token tiles; 512 tokens (mean 64) 133 and 120; 1024 tokens 192 on 128-token
+// and 197 on 256-token tiles, 2048 tokens 312 and 284.
+int moe_tile16_tokens(int64_t T, int64_t E, int64_t topk)
 {
     const int64_t mean = T * topk / E;
-    // 32-bit byte offsets into the activations and into 256 rows of h
-    if (mean < 2 || T * H * 2 >= (1ll << 32) || !tiles16_fit(H) || !tiles16_fit(I))
-        return 0;
-    return mean <= 24 ? 32 : mean < 160 ? 128 : 256;
+    return mean < 12 ? 0 : mean <= 40 ? 64 : mean < 160 ? 128 : 256;
 }
 
 hipError_t launch_moe_tiles16(const MxMoeArgs &a, int tokens, int max_tiles, hipStream_t st)
 {
     const bool bf = a.type == kBF16;
     switch (tokens) {
-    case 32:
-        return bf ? launch_moe_pair<true, 2, 1, 1, 2, 1, 1, 2>(a, max_tiles, st)
-                  : launch_moe_pair<false, 2, 1, 1, 2, 1, 1, 2>(a, max_tiles, st);
+    case 64:
+        return bf ? launch_moe_pair<true, 2, 2, 1, 2, 1, 1, 3>(a, max_tiles, st)
+                  : launch_moe_pair<false, 2, 2, 1, 2, 1, 1, 3>(a, max_tiles, st);
     case 128:
         return bf ? launch_moe_pair<true, 2, 2, 1, 2, 2, 1, 2>(a, max_tiles, st)
                   : launch_moe_pair<false, 2, 2, 1, 2, 2, 1, 2>(a, max_tiles, st);

@@ -71,6 +71,7 @@ def test_gemm_refusals(L):
     refused(L, f(P, P, P, P, F16, 8, 16, 2, None), "GQ_ESHAPE", "K = 16")
     refused(L, f(P, P, P, P, F16, 8, 64, (1 << 21) + 1, None), "GQ_ESHAPE", "N = ")
     refused(L, f(P, P, P, P, F16, -8, 64, 1, None), "GQ_EINVAL", "M = -8")
+    refused(L, f(P, P, P, P, F16, 8, (1 << 22) + 32, 1, None), "GQ_ESHAPE", "K = ")
     refused(L, f(P, P, P, BAD, BF16, 8, 64, 1, None), "GQ_EALIGN", " y ")
     assert f(None, None, None, None, F16, 8, 64, 0, None) == 0
     g = L.gq_gemm_mxfp4_mxfp4
@@ -100,7 +101,8 @@ def test_moe_refusals(L):
     refused(L, call(k=5), "GQ_EINVAL", "topk = 5")
     refused(L, call(E=300), "GQ_ESHAPE", "E = 300")
     refused(L, call(T=1 << 20), "GQ_ESHAPE", "T*topk")
-    refused(L, call(T=1 << 18, H=1 << 17, n=1 << 62), "GQ_ESHAPE", "2^34")
+    refused(L, call(T=1 << 18, H=1 << 13, n=1 << 62), "GQ_ESHAPE", "T*H")
+    refused(L, call(H=(1 << 22) + 32, n=1 << 62), "GQ_ESHAPE", "H = ")
     refused(L, call(w=[P, P, P, None, P, P]), "GQ_EINVAL", "ws_up is NULL")
     refused(L, call(x=BAD), "GQ_EALIGN", " x ")
     refused(L, call(ws=None), "GQ_EWORKSPACE", str(need))
