@@ -499,120 +499,174 @@ def quantize_q8k(x, stream=None):
 
 # -- microscaled 4-bit (MXFP4): codes uint8 [..][K/2], scales uint8 [..][K/32] -----
 
+# These helpers check their tensors (they are small next to a launch, and a host tensor's
+# address would fault the GPU) and are kept short: a decode step's products take a few
+# microseconds on the device.
+
+_torch = None
+_mx_codes = {}
+
+
+_raw_stream = None
+
+
+def _mx_enter(name, t):
+    """(torch, index of the current device), which t has to be on."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _mx_codes.update({torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16})
+        # the current stream's handle without a Stream object, where torch has it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _torch = torch
+    dev = t.get_device()
+    if dev < 0 or dev != _torch.cuda.current_device():
+        raise ValueError("%s is on %s, not on the current device" % (name, t.device))
+    return _torch, dev
+
+
 def _mx_dtype(dtype, f32=True) -> int:
-    import torch
-    code = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}.get(dtype)
+    code = _mx_codes.get(dtype)
     if code is None or (code == GQ_F32 and not f32):
         raise ValueError("unsupported dtype %s" % dtype)
     return code
 
 
-def _mx_check(name, t, dtype=None, shape=None):
-    """A device tensor of this dtype and shape, on the current device."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _mx_addr(name, t, dev, dtype, shape=None):
+    """Address of a contiguous tensor of this dtype and shape on the current device."""
+    if t.get_device() != dev:
         raise ValueError("%s is on %s, not on the current device" % (name, t.device))
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError("%s is %s, expected %s" % (name, t.dtype, dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    return t
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
-def _mx_planes(name, q, s):
-    """The logical shape (.., rows, K) of an MXFP4 matrix or stack."""
-    import torch
-    _mx_check(name + " codes", q, torch.uint8)
-    K = q.shape[-1] * 2
-    _mx_check(name + " scales", s, torch.uint8, tuple(q.shape[:-1]) + (K // 32,))
-    return tuple(q.shape[:-1]) + (K,)
+def _mx_planes(name, q, s, dev, rank):
+    """(addresses of codes and scales, logical shape [..][rows][K]) of an MXFP4 matrix
+    (rank 2) or stack (rank 3; rank 0: any)."""
+    shape = q.shape
+    if len(shape) != rank and (rank or not len(shape)):
+        raise ValueError("%s codes have %d dimensions, expected %d" % (name, len(shape), rank))
+    bytes_ = shape[-1]
+    return (_mx_addr(name, q, dev, _torch.uint8),
+            _mx_addr(name, s, dev, _torch.uint8, (*shape[:-1], bytes_ >> 4)),
+            (*shape[:-1], 2 * bytes_))
 
 
-def _mx_out(out, shape, dtype, device, stream):
-    """The output: `out` checked, or a new tensor that belongs to the stream of the call."""
-    import torch
-    if out is not None:
-        return _mx_check("out", out, dtype, shape)
+def _mx_stream(stream, dev):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _raw_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _mx_new(shape, dtype, like, stream):
+    """A new tensor that belongs to the stream of the call."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        stream = _torch.cuda.ExternalStream(stream)
+    with _torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _mx_rows(name, x, K):
+    """x [..][K] as [rows][K]."""
+    if x.shape[-1] != K:
+        raise ValueError("%s has rows of %d values, expected %d" % (name, x.shape[-1], K))
+    if x.dim() == 2:
+        return x
+    if not x.is_contiguous(): # (a copy would belong to another stream than the call's)
+        raise ValueError("%s must be contiguous" % name)
+    return x.view(-1, K)
 
 
 def quantize_mxfp4(x, stream=None):
     """x [..][K] (float32, float16 or bfloat16; the last dimension contiguous, a
     two-dimensional x may have strided rows) -> (codes uint8 [..][K/2], scales
     uint8 [..][K/32])."""
-    import torch
+    torch, dev = _mx_enter("x", x)
     code = _mx_dtype(x.dtype)
-    _mx_check("x", x)
-    K = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    if x.dim() == 2 and x.stride(-1) == 1:
-        x2 = x
+    lead, K = x.shape[:-1], x.shape[-1]
+    if not x.is_contiguous() and (x.dim() != 2 or x.stride(1) != 1):
+        raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
+    if x.dim() == 2:
+        N = lead[0]
+        ldx = x.stride(0) if N > 1 else K
     else:
-        if not x.is_contiguous():
-            raise ValueError("x must be contiguous, or two-dimensional with contiguous rows")
-        x2 = x.reshape(-1, K) if x.numel() else x.reshape(0, K)
-    N = x2.shape[0]
-    ldx = x2.stride(0) if N > 1 else K
-    q = _mx_out(None, lead + (K // 2,), torch.uint8, x.device, stream)
-    s = _mx_out(None, lead + (K // 32,), torch.uint8, x.device, stream)
-    gq_quantize_mxfp4(x2, code, ldx, q, s, N, K, stream)
+        N = 1
+        for n in lead:
+            N *= n
+        ldx = K
+    q = _mx_new(lead + (K // 2,), torch.uint8, x, stream)
+    s = _mx_new(lead + (K // 32,), torch.uint8, x, stream)
+    _check(lib().gq_quantize_mxfp4(x.data_ptr(), code, ldx, q.data_ptr(), s.data_ptr(), N, K,
+                                   _mx_stream(stream, dev)))
     return q, s
 
 
 def dequant_mxfp4(q, s, dtype=None, out=None, stream=None):
     """The values of codes [..][K/2] and scales [..][K/32] as float32 (or dtype)."""
-    import torch
-    dtype = torch.float32 if dtype is None else dtype
-    shape = _mx_planes("matrix", q, s)
-    o = _mx_out(out, shape, dtype, q.device, stream)
+    torch, dev = _mx_enter("matrix codes", q)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    qa, sa, shape = _mx_planes("matrix", q, s, dev, 0)
+    code = _mx_dtype(dtype)
+    if out is None:
+        out = _mx_new(shape, dtype, q, stream)
     rows = 1
     for n in shape[:-1]:
         rows *= n
-    gq_dequant_mxfp4(q, s, o, _mx_dtype(dtype), rows, shape[-1], stream)
-    return o
+    _check(lib().gq_dequant_mxfp4(qa, sa, _mx_addr("out", out, dev, dtype, shape), code, rows,
+                                  shape[-1], _mx_stream(stream, dev)))
+    return out
 
 
 def gemv_mxfp4(wq, ws, x, out=None, stream=None):
     """y [B][M] float32 = x [B][K] float32 * W^T for MXFP4 W [M][K], 1 <= B <= 16."""
-    import torch
-    M, K = _mx_planes("W", wq, ws)
-    _mx_check("x", x, torch.float32)
-    x2 = x.reshape(-1, K)
-    B = x2.shape[0]
-    y = _mx_out(out, (B, M), torch.float32, x.device, stream)
-    gq_gemv_mxfp4(wq, ws, x2, y, M, K, B, stream)
+    torch, dev = _mx_enter("x", x)
+    qa, sa, (M, K) = _mx_planes("W", wq, ws, dev, 2)
+    x = _mx_rows("x", x, K)
+    xa = _mx_addr("x", x, dev, torch.float32)
+    B = x.shape[0]
+    y = _mx_new((B, M), torch.float32, x, stream) if out is None else out
+    _check(lib().gq_gemv_mxfp4(qa, sa, xa, _mx_addr("out", y, dev, torch.float32, (B, M)), M, K, B,
+                               _mx_stream(stream, dev)))
     return y
 
 
 def gemm_mxfp4(wq, ws, x, out=None, stream=None):
     """Y [N][M] = X [N][K] * W^T in x's dtype (float16 or bfloat16), MXFP4 W [M][K]."""
-    M, K = _mx_planes("W", wq, ws)
+    _, dev = _mx_enter("x", x)
+    qa, sa, (M, K) = _mx_planes("W", wq, ws, dev, 2)
+    x = _mx_rows("x", x, K)
     code = _mx_dtype(x.dtype, f32=False)
-    _mx_check("x", x)
-    x2 = x.reshape(-1, K)
-    N = x2.shape[0]
-    y = _mx_out(out, (N, M), x.dtype, x.device, stream)
-    gq_gemm_mxfp4(wq, ws, x2, y, code, M, K, N, stream)
+    xa = _mx_addr("x", x, dev, x.dtype)
+    N = x.shape[0]
+    y = _mx_new((N, M), x.dtype, x, stream) if out is None else out
+    _check(lib().gq_gemm_mxfp4(qa, sa, xa, _mx_addr("out", y, dev, x.dtype, (N, M)), code, M, K, N,
+                               _mx_stream(stream, dev)))
     return y
 
 
 def gemm_mxfp4_mxfp4(wq, ws, xq, xs, dtype=None, out=None, stream=None):
     """Y [N][M] = X * W^T of two MXFP4 matrices, X [N][K] from quantize_mxfp4; Y is
     float32 unless dtype (or out) says otherwise."""
-    import torch
+    torch, dev = _mx_enter("X codes", xq)
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
-    M, K = _mx_planes("W", wq, ws)
-    N, KX = _mx_planes("X", xq, xs)
+    code = _mx_dtype(dtype)
+    qa, sa, (M, K) = _mx_planes("W", wq, ws, dev, 2)
+    xqa, xsa, (N, KX) = _mx_planes("X", xq, xs, dev, 2)
     if KX != K:
         raise ValueError("X has rows of %d values, W of %d" % (KX, K))
-    y = _mx_out(out, (N, M), dtype, xq.device, stream)
-    gq_gemm_mxfp4_mxfp4(wq, ws, xq, xs, y, _mx_dtype(dtype), M, K, N, stream)
+    y = _mx_new((N, M), dtype, xq, stream) if out is None else out
+    _check(lib().gq_gemm_mxfp4_mxfp4(qa, sa, xqa, xsa, _mx_addr("out", y, dev, dtype, (N, M)), code,
+                                     M, K, N, _mx_stream(stream, dev)))
     return y
 
 
@@ -621,22 +675,26 @@ def moe_mxfp4(w_gate, w_up, w_down, x, topk_ids, topk_w, ws=None, out=None, stre
     """Mixture-of-experts feed-forward over MXFP4 stacks, each a pair (codes, scales):
     gate and up [E][I][H], down [E][H][I]; x [T][H] float16 or bfloat16.  Returns
     (out [T][H] in x's dtype, workspace)."""
-    import torch
-    E, I, H = _mx_planes("w_gate", *w_gate)
-    if _mx_planes("w_up", *w_up) != (E, I, H):
+    torch, dev = _mx_enter("x", x)
+    gq_, gs, shape = _mx_planes("w_gate", *w_gate, dev, 3)
+    E, I, H = shape
+    uq, us, up_shape = _mx_planes("w_up", *w_up, dev, 3)
+    dq, ds, down_shape = _mx_planes("w_down", *w_down, dev, 3)
+    if up_shape != shape:
         raise ValueError("w_up differs from w_gate in shape")
-    if _mx_planes("w_down", *w_down) != (E, H, I):
+    if down_shape != (E, H, I):
         raise ValueError("w_down is not [E][H][I]")
     code = _mx_dtype(x.dtype, f32=False)
     T, topk = topk_ids.shape
-    _mx_check("x", x, shape=(T, H))
-    _mx_check("topk_ids", topk_ids, torch.int32)
-    _mx_check("topk_w", topk_w, torch.float32, (T, topk))
-    need = gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk)
+    xa = _mx_addr("x", x, dev, x.dtype, (T, H))
+    ia = _mx_addr("topk_ids", topk_ids, dev, torch.int32)
+    wa = _mx_addr("topk_w", topk_w, dev, torch.float32, (T, topk))
     if ws is None:
-        ws = _mx_out(None, (max(need, 16),), torch.uint8, x.device, stream)
-    _mx_check("ws", ws)
-    o = _mx_out(out, (T, H), x.dtype, x.device, stream)
-    gq_moe_gemm_mxfp4(*w_gate, *w_up, *w_down, x, topk_ids, topk_w, o, code, T, H, I, E, topk,
-                      input_weighted, ws, stream=stream)
+        need = gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk)
+        ws = _mx_new((max(need, 16),), torch.uint8, x, stream)
+    o = _mx_new((T, H), x.dtype, x, stream) if out is None else out
+    _check(lib().gq_moe_gemm_mxfp4(gq_, gs, uq, us, dq, ds, xa, ia, wa,
+                                   _mx_addr("out", o, dev, x.dtype, (T, H)), code, T, H, I, E, topk,
+                                   int(input_weighted), _mx_addr("ws", ws, dev, ws.dtype),
+                                   ws.numel() * ws.element_size(), _mx_stream(stream, dev)))
     return o, ws
