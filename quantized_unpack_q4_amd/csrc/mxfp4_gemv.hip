@@ -8,17 +8,19 @@
 // Binary32 activations are split into three bfloat16 parts, x = a + b + c exactly
 // (8 + 8 + 8 significant bits, each part cut toward zero from what is left), and an
 // MXFP4 weight is a bfloat16 number exactly (s <= 252), so the products are exact and
-// only the binary32 sums of the matrix cores round.  Infinite and NaN activations stay
-// in the first part alone.
+// only the binary32 sums of the matrix cores round.  An infinite or NaN activation leaves a
+// NaN in the second part (infinity minus infinity), so its row's results are NaN.
 //
-// A workgroup of NW waves owns RT tiles of 16 weight rows; its waves take every NW-th
-// step of 128 columns and join their sums through LDS in wave order.  The parts of a
-// chunk of x (1024 NW values, all rows of it) lie in LDS as rows of bfloat16.  In a step
-// lane (c, h) takes block h of weight row c, converted with its scale, and feeds four
-// 16x16x32 products whose k order is permuted alike for both operands (product i takes
-// columns 8i .. 8i+7 of the step's four blocks).  Up to five activation rows the three
-// parts of a row are three columns of one product (column 3b + p), added at the end;
-// above that each part has a product of its own.
+// In a step of 128 columns lane (c, h) takes block h of weight row c, converted with its
+// scale, and feeds four 16x16x32 products whose k order is permuted alike for both operands
+// (product i takes columns 8i .. 8i+7 of the step's four blocks).  A workgroup of NW waves
+// owns RT tiles of 16 weight rows; its waves take units of Q consecutive steps, every NW-th,
+// and join their sums through LDS in wave order.
+//
+// Up to five activation rows the three parts of a row are three columns of one product
+// (column 3b + p), added at the end: the parts of a chunk of x (1024 NW values, all rows of
+// it) lie in LDS as rows of bfloat16, split once for the workgroup.  Above five rows each
+// part has a product of its own and every wave splits what it needs itself.
 #include "gq_internal.h"
 #include "mxfp4_device.h"
 
@@ -30,7 +32,7 @@ namespace {
 // thread: this many columns, whole steps of 128.  Their parts take 3 B rows of two bytes a
 // column and 16 more, at most x_bytes(NW).
 __host__ __device__ constexpr int chunk_columns(int NW, int B) { return 1024 * NW / B / 128 * 128; }
-constexpr int x_bytes(int NW) { return 6 * 1024 * NW + 48 * 16; }
+constexpr int x_bytes(int NW) { return 6 * 1024 * NW + 15 * 16; }
 
 // The three bfloat16 parts of four binary32 values, packed.
 __device__ __forceinline__ void split3(const float4 v, uint2 &a, uint2 &b, uint2 &c)
@@ -43,10 +45,6 @@ __device__ __forceinline__ void split3(const float4 v, uint2 &a, uint2 &b, uint2
         const float r = x[j] - __builtin_bit_cast(float, hi[j] & 0xffff0000u);
         mid[j] = __builtin_bit_cast(uint32_t, r);
         lo[j] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, mid[j] & 0xffff0000u));
-        if ((hi[j] & 0x7f800000u) == 0x7f800000u) {
-            hi[j] |= (hi[j] & 0x7fffffu) ? 0x400000u : 0u; // a NaN stays one when cut
-            mid[j] = lo[j] = 0;
-        }
     }
     // the upper halves of a pair
     a = make_uint2(__builtin_amdgcn_perm(hi[1], hi[0], 0x07060302u),
@@ -57,13 +55,12 @@ __device__ __forceinline__ void split3(const float4 v, uint2 &a, uint2 &b, uint2
                    __builtin_amdgcn_perm(lo[3], lo[2], 0x07060302u));
 }
 
-// SETS 1: 3 B <= 16; SETS 3: B <= 16.
-template <int SETS, int RT, int NW>
+// 1 <= B <= 5.
+template <int RT, int NW, int Q>
 __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const float *__restrict__ x,
                                                              float *__restrict__ y, int M, int K,
                                                              int B)
 {
-    constexpr int GS = 4 / RT; // steps per group of loads, two groups in registers
     __shared__ __attribute__((aligned(16))) uint8_t lds[x_bytes(NW)];
     static_assert(NW * RT * 1024 <= x_bytes(NW), "sums fit");
     const int tid = threadIdx.x, lane = tid & 63;
@@ -71,8 +68,8 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const floa
     const int c = lane & 15, h = lane >> 4;
     const int m0 = blockIdx.x * (16 * RT);
     const int nblk = K >> 5, steps = (nblk + 3) >> 2;
-    const int kc = chunk_columns(NW, B), cs = kc >> 7, spc = (cs + NW - 1) / NW;
-    const int chunks = (steps + cs - 1) / cs, total = chunks * spc;
+    const int kc = chunk_columns(NW, B), cs = kc >> 7, upc = (cs + Q * NW - 1) / (Q * NW);
+    const int chunks = (steps + cs - 1) / cs, total = chunks * upc;
     const int xstride = 2 * kc + 16;
 
     const uint8_t *qrow[RT], *srow[RT];
@@ -82,41 +79,43 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const floa
         qrow[t] = w.q + row * (K >> 1);
         srow[t] = w.s + row * nblk;
     }
-    // this wave's steps: spc in every chunk, at first (in the chunk) = its number and then
-    // every NW-th; not all of them exist
+    // this wave's units: upc in every chunk, at first (in the chunk) = its number and then
+    // every NW-th; not all of their steps exist
     struct Walk {
-        int n = 0, first = 0; // steps taken in this chunk, its first step
-    };
-    auto step_of = [&](const Walk &k) {
-        const int in = wave + NW * k.n, st = k.first + in;
-        return in < cs && st < steps ? st : -1;
+        int n = 0, first = 0; // units taken in this chunk, the chunk's first step
     };
     auto next = [&](Walk &k) {
-        if (++k.n == spc) {
+        if (++k.n == upc) {
             k.n = 0;
             k.first += cs;
         }
     };
-    Walk ahead, now;
-    struct Group {
-        uint4 q[GS][RT];
-        uint32_t s[GS][RT];
+    // step u of the unit, in the chunk; -1: none
+    auto step_of = [&](const Walk &k, int u) {
+        const int in = Q * (wave + NW * k.n) + u;
+        return in < cs && k.first + in < steps ? in : -1;
     };
-    auto load = [&](Group &g) {
+    Walk ahead, now;
+    struct Unit {
+        uint4 q[Q][RT];
+        MxScales<Q> s[RT];
+    };
+    auto load = [&](Unit &g) {
+        const int b0 = 4 * (ahead.first + Q * (wave + NW * ahead.n));
+        if (step_of(ahead, 0) >= 0) {
 #pragma unroll
-        for (int u = 0; u < GS; ++u) {
-            const int st = step_of(ahead);
-            next(ahead);
-            if (st < 0)
-                continue;
-            const bool ok = 4 * st + h < nblk; // past the last block: zeros of scale 1
-            const int blk = ok ? 4 * st + h : nblk - 1;
+            for (int u = 0; u < Q; ++u) {
+                // past the last block: that one again, taken as zeros
+                const int blk = min(b0 + 4 * u + h, nblk - 1);
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                g.q[u][t] = ld16(qrow[t] + 16 * (int64_t)blk);
-                g.s[u][t] = srow[t][blk];
+                for (int t = 0; t < RT; ++t)
+                    g.q[u][t] = ld16(qrow[t] + 16 * blk);
             }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                g.s[t].load(srow[t], b0, nblk);
         }
+        next(ahead);
     };
     float4 xr[4];
     auto load_x = [&](int ch) {
@@ -139,11 +138,10 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const floa
                 continue;
             uint2 p0, p1, p2;
             split3(xr[j], p0, p1, p2);
-            uint8_t *d = lds + (SETS == 1 ? 3 * b : b) * xstride + 8 * (f - b * kq);
-            const int ps = (SETS == 1 ? 1 : B) * xstride;
+            uint8_t *d = lds + 3 * b * xstride + 8 * (f - b * kq);
             *reinterpret_cast<uint2 *>(d) = p0;
-            *reinterpret_cast<uint2 *>(d + ps) = p1;
-            *reinterpret_cast<uint2 *>(d + 2 * ps) = p2;
+            *reinterpret_cast<uint2 *>(d + xstride) = p1;
+            *reinterpret_cast<uint2 *>(d + 2 * xstride) = p2;
         }
     };
 
@@ -152,63 +150,56 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const floa
     for (int t = 0; t < RT; ++t)
         acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
     // columns past the last repeat it and are not stored
-    const int xrow = SETS == 1 ? min(c, 3 * B - 1) : min(c, B - 1);
-    auto compute = [&](int u, Group &g) {
-        const int st = step_of(now);
-        if (st < 0) // the whole wave
-            return;
-        const bool ok = 4 * st + h < nblk;
-        const uint8_t *xp = lds + xrow * xstride + 64 * h + 256 * (st - now.first);
-        float sc[RT];
+    const int xrow = min(c, 3 * B - 1);
+    auto compute = [&](Unit &g) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            sc[t] = mx_scale(ok ? g.s[u][t] : 127u);
-            if (!ok)
-                g.q[u][t] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint4 xv[SETS];
-#pragma unroll
-            for (int p = 0; p < SETS; ++p)
-                xv[p] = ld16(xp + p * B * xstride + 16 * n);
+        for (int u = 0; u < Q; ++u) {
+            const int in = step_of(now, u);
+            if (in < 0) // the whole wave
+                break;
+            const bool ok = 4 * (now.first + in) + h < nblk;
+            const uint8_t *xp = lds + xrow * xstride + 64 * h + 256 * in;
+            float sc[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const uint4 &q = g.q[u][t];
-                const uint4 wv = mx_values8<true>(n == 0 ? q.x : n == 1 ? q.y : n == 2 ? q.z : q.w, sc[t]);
+                sc[t] = mx_scale((g.s[t].w[u] >> (8 * h)) & 255u);
+                if (!ok)
+                    g.q[u][t] = make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-                for (int p = 0; p < SETS; ++p)
-                    acc[t] = mx_mfma16<true>(wv, xv[p], acc[t]);
+            for (int n = 0; n < 4; ++n) {
+                const uint4 xv = ld16(xp + 16 * n);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const uint4 &q = g.q[u][t];
+                    const uint4 wv = mx_values8<true>(n == 0 ? q.x : n == 1 ? q.y : n == 2 ? q.z : q.w, sc[t]);
+                    acc[t] = mx_mfma16<true>(wv, xv, acc[t]);
+                }
             }
         }
+        next(now);
     };
 
-    Group g0, g1;
+    Unit g0, g1;
     load(g0);
     load_x(0);
     int chunk = 0;
-    auto half = [&](int i0, Group &cur, Group &nxt) {
+    auto half = [&](Unit &cur, Unit &nxt) {
         load(nxt);
-#pragma unroll
-        for (int u = 0; u < GS; ++u) {
-            const int i = i0 + u;
-            if (i >= total)
-                break;
-            if (now.n == 0) { // the first step of a chunk, for all waves alike
-                if (chunk > 0)
-                    __syncthreads(); // the chunk before has been read
-                stage_x();
-                if (++chunk < chunks)
-                    load_x(chunk);
-                __syncthreads();
-            }
-            compute(u, cur);
-            next(now);
+        if (now.n == 0) { // the first unit of a chunk, for all waves alike
+            if (chunk > 0)
+                __syncthreads(); // the chunk before has been read
+            stage_x();
+            if (++chunk < chunks)
+                load_x(chunk);
+            __syncthreads();
         }
+        compute(cur);
     };
-    for (int i = 0; i < total; i += 2 * GS) {
-        half(i, g0, g1);
-        half(i + GS, g1, g0);
+    for (int i = 0; i < total; i += 2) {
+        half(g0, g1);
+        if (i + 1 < total)
+            half(g1, g0);
     }
 
     // lane l of a wave holds rows 4 (l / 16) + 0..3 of column l % 16
@@ -227,20 +218,159 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_kernel(MxMat w, const floa
         float sum = 0.f;
         for (int v = 0; v < NW; ++v) {
             const float *fv = f + v * RT * 256;
-            if constexpr (SETS == 1)
-                sum += (fv[4 * (3 * b + 2)] + fv[4 * (3 * b + 1)]) + fv[4 * (3 * b)];
-            else
-                sum += fv[4 * b];
+            sum += (fv[4 * (3 * b + 2)] + fv[4 * (3 * b + 1)]) + fv[4 * (3 * b)];
         }
         y[(int64_t)b * M + m0 + r] = sum;
     }
 }
 
-template <int SETS, int RT, int NW>
+// More than five activation rows: a wave splits what it needs of x itself.  In a unit of two
+// steps it loads 256 columns of the B rows (1 KB of a row per load), turns them in LDS of its
+// own (rows padded by 16 bytes, so that the 16 rows of a read phase meet 16 distinct bank
+// groups) and splits the eight values a lane feeds to a product: no barriers, and the loads
+// of the next unit are in flight meanwhile.
+template <int RT, int NW>
+__global__ __launch_bounds__(64 * NW) void mxfp4_gemv_wide_kernel(MxMat w, const float *__restrict__ x,
+                                                                  float *__restrict__ y, int M,
+                                                                  int K, int B)
+{
+    constexpr int Q = 2, kRow = 1024 + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[NW][16 * kRow];
+    static_assert(RT * 1024 <= 16 * kRow, "sums fit");
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int m0 = blockIdx.x * (16 * RT);
+    const int nblk = K >> 5, units = (nblk + 4 * Q - 1) / (4 * Q);
+
+    const uint8_t *qrow[RT], *srow[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) { // rows past the last repeat it and are not stored
+        const int64_t row = min(m0 + 16 * t + c, M - 1);
+        qrow[t] = w.q + row * (K >> 1);
+        srow[t] = w.s + row * nblk;
+    }
+    struct Unit {
+        uint4 q[Q][RT];
+        MxScales<Q> s[RT];
+    };
+    auto load = [&](int un, Unit &g) {
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+            // past the last block: that one again, taken as zeros
+            const int blk = min(4 * (Q * un + u) + h, nblk - 1);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                g.q[u][t] = ld16(qrow[t] + 16 * blk);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+            g.s[t].load(srow[t], 4 * Q * un, nblk);
+    };
+    float4 xr[16];
+    auto load_x = [&](int un) {
+        const int k = 256 * un + 4 * lane;
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            if (b < B)
+                xr[b] = k < K ? ldf4(x + (int64_t)b * K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto turn_x = [&]() {
+        uint8_t *d = lds[wave] + 16 * lane;
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            if (b < B)
+                *reinterpret_cast<float4 *>(d + b * kRow) = xr[b];
+    };
+
+    float4_t acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    // columns past the last repeat it and are not stored
+    const uint8_t *xp = lds[wave] + min(c, B - 1) * kRow + 128 * h;
+    auto compute = [&](int un, Unit &g) {
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+            const bool ok = 4 * (Q * un + u) + h < nblk;
+            float sc[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                sc[t] = mx_scale((g.s[t].w[u] >> (8 * h)) & 255u);
+                if (!ok)
+                    g.q[u][t] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float *v = reinterpret_cast<const float *>(xp + 512 * u + 32 * n);
+                uint2 a0, b0, c0, a1, b1, c1;
+                split3(ldf4(v), a0, b0, c0);
+                split3(ldf4(v + 4), a1, b1, c1);
+                const uint4 xa = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                const uint4 xb = make_uint4(b0.x, b0.y, b1.x, b1.y);
+                const uint4 xc = make_uint4(c0.x, c0.y, c1.x, c1.y);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const uint4 &q = g.q[u][t];
+                    const uint4 wv = mx_values8<true>(n == 0 ? q.x : n == 1 ? q.y : n == 2 ? q.z : q.w, sc[t]);
+                    acc[t] = mx_mfma16<true>(wv, xc, acc[t]);
+                    acc[t] = mx_mfma16<true>(wv, xb, acc[t]);
+                    acc[t] = mx_mfma16<true>(wv, xa, acc[t]);
+                }
+            }
+        }
+    };
+
+    Unit g0, g1;
+    int un = wave;
+    if (un < units) {
+        load(un, g0);
+        load_x(un);
+    }
+    auto half = [&](Unit &cur, Unit &nxt) {
+        turn_x();
+        if (un + NW < units) {
+            load(un + NW, nxt);
+            load_x(un + NW);
+        }
+        compute(un, cur);
+        un += NW;
+    };
+    while (un < units) {
+        half(g0, g1);
+        if (un < units)
+            half(g1, g0);
+    }
+
+    // lane l of a wave holds rows 4 (l / 16) + 0..3 of column l % 16
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        *reinterpret_cast<float4_t *>(lds[wave] + 1024 * t + 16 * lane) = acc[t];
+    __syncthreads();
+    for (int o = tid; o < RT * 16 * B; o += 64 * NW) {
+        const int r = o % (16 * RT), b = o / (16 * RT), m = r & 15;
+        if (m0 + r >= M)
+            continue;
+        float sum = 0.f;
+        for (int v = 0; v < NW; ++v)
+            sum += reinterpret_cast<const float *>(lds[v])[256 * (r >> 4) + 64 * (m >> 2) + 4 * b + (m & 3)];
+        y[(int64_t)b * M + m0 + r] = sum;
+    }
+}
+
+template <int RT, int NW, int Q>
 hipError_t launch(MxMat w, const float *x, float *y, int64_t M, int64_t K, int B, hipStream_t st)
 {
-    hipLaunchKernelGGL((mxfp4_gemv_kernel<SETS, RT, NW>), dim3((unsigned)((M + 16 * RT - 1) / (16 * RT))),
+    hipLaunchKernelGGL((mxfp4_gemv_kernel<RT, NW, Q>), dim3((unsigned)((M + 16 * RT - 1) / (16 * RT))),
                        dim3(64 * NW), 0, st, w, x, y, (int)M, (int)K, B);
+    return hipGetLastError();
+}
+
+template <int RT>
+hipError_t launch_wide(MxMat w, const float *x, float *y, int64_t M, int64_t K, int B, hipStream_t st)
+{
+    hipLaunchKernelGGL((mxfp4_gemv_wide_kernel<RT, 8>), dim3((unsigned)((M + 16 * RT - 1) / (16 * RT))),
+                       dim3(512), 0, st, w, x, y, (int)M, (int)K, B);
     return hipGetLastError();
 }
 
@@ -249,22 +379,23 @@ hipError_t launch(MxMat w, const float *x, float *y, int64_t M, int64_t K, int B
 hipError_t launch_gemv_mxfp4(MxMat w, const float *x, float *y, int64_t M, int64_t K, int B,
                              hipStream_t st)
 {
-    // Tiles of 16 rows shared out among the CUs, up to four to a workgroup (the
-    // activations are split once for them).  Eight waves where two or three such
-    // workgroups share a CU or all of x is staged at once, sixteen where one has a CU to
-    // itself.  Measured, us, K-split over 8 and 16 waves: 4096 x 4096 batch 1 6.7, 7.9,
-    // batch 16 17.0, 14.7; 4096 x 14336 batch 1 16.7, 15.4, batch 16 54, 44; 14336 x 4096
-    // with four tiles a workgroup batch 1 14.3, 16.8 (one tile: 15.0, 26), batch 16 26.5,
-    // 29.9 (one tile: 43, 50); with two tiles batch 4 15.9, 18.2, batch 16 38, 31.5.
+    // Tiles of 16 rows shared out among the CUs (the activations are split once for a
+    // workgroup's or wave's).  Measured, us.  Up to five rows, one tile of 8 waves, of 16
+    // waves, two tiles of 8 waves: 4096 x 4096 batch 1 5.6, 6.3, 7.5, batch 4 7.0, 6.3, 8.5;
+    // 4096 x 14336 batch 1 12.5, 11.5, 18; 14336 x 4096 batch 1 12.1, 20, 12.0, batch 4 16, 20,
+    // 13.7; units of four, two and one steps 4096 x 4096 batch 1 5.6, 6.3, 7.5.  More rows, one,
+    // two and four tiles: 4096 x 14336 batch 16 27, 32, 46 (parts staged for all waves: 30);
+    // 6144 x 4096 18, 12.6, 16.5 (13.6); 14336 x 4096 34, 23, 18 (23).
     const int64_t tiles = (M + 15) / 16, cus = device_cus();
-    const bool columns = 3 * B <= 16;
-    if (tiles > 2 * cus)
-        return columns ? launch<1, 4, 8>(w, x, y, M, K, B, st) : launch<3, 4, 8>(w, x, y, M, K, B, st);
+    if (B > 5)
+        return tiles > 2 * cus ? launch_wide<4>(w, x, y, M, K, B, st)
+               : tiles > cus   ? launch_wide<2>(w, x, y, M, K, B, st)
+                               : launch_wide<1>(w, x, y, M, K, B, st);
     if (tiles > cus)
-        return columns ? launch<1, 2, 8>(w, x, y, M, K, B, st) : launch<3, 2, 16>(w, x, y, M, K, B, st);
-    if (!columns)
-        return launch<3, 1, 16>(w, x, y, M, K, B, st);
-    return B * K <= 8192 ? launch<1, 1, 8>(w, x, y, M, K, B, st) : launch<1, 1, 16>(w, x, y, M, K, B, st);
+        return launch<2, 8, 2>(w, x, y, M, K, B, st);
+    if (B * K > 8192) // x is not staged at once by eight waves
+        return launch<1, 16, 2>(w, x, y, M, K, B, st);
+    return K >= 4096 ? launch<1, 8, 4>(w, x, y, M, K, B, st) : launch<1, 8, 2>(w, x, y, M, K, B, st);
 }
 
 } // namespace gq

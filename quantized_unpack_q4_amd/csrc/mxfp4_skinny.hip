@@ -38,12 +38,11 @@ struct SkinnyArgs {
     int weight_input;
 };
 
-// R tiles of 16 weight rows (gate/up: of each matrix).
-template <int ACT, int MODE, int R, int NW>
+// R tiles of 16 weight rows (gate/up: of each matrix); a wave takes Q steps of K at a time.
+template <int ACT, int MODE, int R, int NW, int Q>
 __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
 {
     constexpr int NMAT = MODE == kGateUp ? 2 : 1, NR = NMAT * R;
-    constexpr int U = NR > 2 ? 8 / NR : 4; // steps whose loads are issued together
     constexpr int NX = ACT == kActMx ? 1 : 4;
     constexpr bool BF = ACT != kActF16;
     __shared__ float4_t red[NW][NR][64];
@@ -63,75 +62,97 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
     }
 
     // rows past the last repeat it and are not stored; tile i of matrix m is NMAT i + m
+    const int nblk = K >> 5;
     const uint8_t *qrow[NR], *srow[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const MxMat &w = i % NMAT ? p.w2 : p.w;
         const int64_t row = min(m0 + 16 * (i / NMAT) + c, M - 1);
         qrow[i] = w.q + e * p.eq + row * (K >> 1);
-        srow[i] = w.s + e * p.es + row * (K >> 5);
+        srow[i] = w.s + e * p.es + row * nblk;
     }
     const int nl = n0 + min(c, nvalid - 1);
     const int64_t xrow = MODE == kGateUp ? p.sorted[nl] / p.topk : nl;
 
+    struct Unit {
+        uint4 q[Q][NR], x[Q][NX];
+        MxScales<Q> s[NR], sx;
+    };
+    auto load = [&](int un, Unit &b) {
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+            // past the last block: that one again, taken as zeros
+            const int blk = min(4 * (Q * un + u) + h, nblk - 1);
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                b.q[u][i] = ld16(qrow[i] + 16 * blk);
+            if constexpr (ACT == kActMx) {
+                b.x[u][0] = ld16(reinterpret_cast<const uint8_t *>(p.x) + xrow * (K >> 1) + 16 * blk);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NX; ++n)
+                    b.x[u][n] = ld16(reinterpret_cast<const uint16_t *>(p.x) + xrow * K + 32 * blk + 8 * n);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            b.s[i].load(srow[i], 4 * Q * un, nblk);
+        if constexpr (ACT == kActMx)
+            b.sx.load(p.xs + xrow * nblk, 4 * Q * un, nblk);
+    };
     float4_t acc[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
         acc[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-
-    const int nblk = K >> 5, steps = (nblk + 3) >> 2;
-    for (int st0 = wave; st0 < steps; st0 += NW * U) {
-        uint4 q[U][NR], xv[U][NX];
-        uint32_t s[U][NR], sx[U];
+    auto compute = [&](int un, Unit &b) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int st = st0 + NW * u;
-            if (st >= steps)
-                break;
-            // past the last block: that one again, taken as zeros of scale 1
-            const int blk = min(4 * st + h, nblk - 1);
+        for (int u = 0; u < Q; ++u) {
+            const bool none = 4 * (Q * un + u) + h >= nblk;
+            if (none) {
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                q[u][i] = ld16(qrow[i] + 16 * blk);
-                s[u][i] = srow[i][blk];
-            }
-            if constexpr (ACT == kActMx) {
-                xv[u][0] = ld16(reinterpret_cast<const uint8_t *>(p.x) + xrow * (K >> 1) + 16 * blk);
-                sx[u] = p.xs[xrow * nblk + blk];
-            } else {
+                for (int i = 0; i < NR; ++i)
+                    b.q[u][i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int n = 0; n < NX; ++n)
-                    xv[u][n] = ld16(reinterpret_cast<const uint16_t *>(p.x) + xrow * K + 32 * blk + 8 * n);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int st = st0 + NW * u;
-            if (st >= steps)
-                break;
-            if (4 * st + h >= nblk) {
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    q[u][i] = make_uint4(0, 0, 0, 0);
-                    s[u][i] = 127;
-                }
-#pragma unroll
-                for (int n = 0; n < NX; ++n)
-                    xv[u][n] = make_uint4(0, 0, 0, 0);
-                sx[u] = 127;
+                    b.x[u][n] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
+                const uint32_t s = b.s[i].w[u] >> (8 * h); // (its low byte)
                 if constexpr (ACT == kActMx) {
-                    acc[i] = mx_mfma16_fp4(q[u][i], s[u][i], xv[u][0], sx[u], acc[i]);
+                    acc[i] = mx_mfma16_fp4(b.q[u][i], s, b.x[u][0], b.sx.w[u] >> (8 * h), acc[i]);
                 } else {
-                    const float sc = mx_scale(s[u][i]);
-                    const uint32_t d[4] = {q[u][i].x, q[u][i].y, q[u][i].z, q[u][i].w};
+                    const float sc = mx_scale(s & 255u);
+                    const uint32_t d[4] = {b.q[u][i].x, b.q[u][i].y, b.q[u][i].z, b.q[u][i].w};
 #pragma unroll
                     for (int n = 0; n < NX; ++n)
-                        acc[i] = mx_mfma16<BF>(mx_values8<BF>(d[n], sc), xv[u][n], acc[i]);
+                        acc[i] = mx_mfma16<BF>(mx_values8<BF>(d[n], sc), b.x[u][n], acc[i]);
                 }
             }
+        }
+    };
+
+    const int units = ((nblk + 3) / 4 + Q - 1) / Q;
+    if constexpr (Q * (NR + NX) <= 20) { // registers for the next unit's loads too
+        Unit b0, b1;
+        int un = wave;
+        if (un < units)
+            load(un, b0);
+        for (; un < units; un += 2 * NW) {
+            if (un + NW < units)
+                load(un + NW, b1);
+            compute(un, b0);
+            if (un + NW < units) {
+                if (un + 2 * NW < units)
+                    load(un + 2 * NW, b0);
+                compute(un + NW, b1);
+            }
+        }
+    } else {
+        for (int un = wave; un < units; un += NW) {
+            Unit b;
+            load(un, b);
+            compute(un, b);
         }
     }
 
@@ -162,11 +183,22 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
     }
 }
 
-template <int ACT, int MODE, int R, int NW>
+// As many steps at a time, up to QMAX, as leave every wave some.
+template <int ACT, int MODE, int R, int NW, int QMAX>
 hipError_t launch(const SkinnyArgs &p, unsigned gy, hipStream_t st)
 {
-    const dim3 grid((unsigned)((p.M + 16 * R - 1) / (16 * R)), gy);
-    hipLaunchKernelGGL((mxfp4_skinny_kernel<ACT, MODE, R, NW>), grid, dim3(64 * NW), 0, st, p);
+    const dim3 grid((unsigned)((p.M + 16 * R - 1) / (16 * R)), gy), block(64 * NW);
+    const int steps = (p.K + 127) / 128;
+    if constexpr (QMAX >= 4) {
+        if (steps >= 4 * NW) {
+            hipLaunchKernelGGL((mxfp4_skinny_kernel<ACT, MODE, R, NW, 4>), grid, block, 0, st, p);
+            return hipGetLastError();
+        }
+    }
+    if (steps >= 2 * NW)
+        hipLaunchKernelGGL((mxfp4_skinny_kernel<ACT, MODE, R, NW, 2>), grid, block, 0, st, p);
+    else
+        hipLaunchKernelGGL((mxfp4_skinny_kernel<ACT, MODE, R, NW, 1>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 
@@ -184,28 +216,26 @@ hipError_t launch_dense(MxMat w, const void *x, const uint8_t *xs, void *y, int 
     p.M = (int)M;
     p.K = (int)K;
     p.N = (int)N;
-    // row tiles shared out among the CUs, up to four to a workgroup (the activations are
+    // Row tiles shared out among the CUs, up to four to a workgroup (the activations are
     // read once for them).  Measured, us at one, two and four: bfloat16 by 16 rows 4096 x
-    // 4096 8.5, 10.3, 14.4; 14336 x 4096 24, 19, 15; 4096 x 14336 23, 30, 43; by 1 row 14336 x
-    // 4096 14.0, 13.7, 13.1; MXFP4 by 16 rows 14336 x 4096 16.9, 13.6, 12.8
+    // 4096 7.8, 9.2, 12.2; 14336 x 4096 26, 17, 13.4; 4096 x 14336 21, 26, 36; by 1 row 14336 x
+    // 4096 15.7, 11.6, 11.0; MXFP4 by 16 rows 14336 x 4096 12.6, 12.4, 10.6.  Four, two and
+    // one step at a time: bfloat16 by 1 row 14336 x 14336 29, 31, 37.
     const int64_t tiles = (M + 15) / 16, cus = device_cus();
-    return tiles > 2 * cus ? launch<ACT, kDense, 4, 8>(p, 1, st)
-           : tiles > cus   ? launch<ACT, kDense, 2, 8>(p, 1, st)
-                           : launch<ACT, kDense, 1, 8>(p, 1, st);
+    return tiles > 2 * cus ? launch<ACT, kDense, 4, 8, 4>(p, 1, st)
+           : tiles > cus   ? launch<ACT, kDense, 2, 8, 4>(p, 1, st)
+                           : launch<ACT, kDense, 1, 8, 4>(p, 1, st);
 }
 
-// One expert product, weights streamed once per 16 tokens.  Two or four row tiles a
-// workgroup of four waves: four once that still gives every CU one.  Measured, us for the
-// layer of 64 experts, top-8, hidden 2048, intermediate 1024 with one tile (eight waves), two
-// and four: 1 token 33, 24, 28; 4 tokens 67, 44, 43; 32 tokens -, 78, 71.
+// One expert product, weights streamed once per 16 tokens: two row tiles a workgroup of four
+// waves, up to two steps at a time.  Measured, us for the layer of 64 experts, top-8, hidden
+// 2048, intermediate 1024, weights from HBM: 1 token 22.5 (one tile 22.9, four 26), 4 tokens
+// 41 (37, 41), 16 tokens 68 (67, 70), 64 tokens 78 (85, 75); with eight waves 26, 54, 93, 109.
 template <int MODE>
-hipError_t launch_expert(const SkinnyArgs &p, bool bf16, int64_t A, hipStream_t st)
+hipError_t launch_expert(const SkinnyArgs &p, bool bf16, hipStream_t st)
 {
     const unsigned gy = (unsigned)p.max_tiles;
-    const int64_t hit = A < p.E ? A : p.E; // experts with a token, at most
-    if ((p.M + 63) / 64 * hit > device_cus())
-        return bf16 ? launch<kActBF16, MODE, 4, 4>(p, gy, st) : launch<kActF16, MODE, 4, 4>(p, gy, st);
-    return bf16 ? launch<kActBF16, MODE, 2, 4>(p, gy, st) : launch<kActF16, MODE, 2, 4>(p, gy, st);
+    return bf16 ? launch<kActBF16, MODE, 2, 4, 2>(p, gy, st) : launch<kActF16, MODE, 2, 4, 2>(p, gy, st);
 }
 
 hipError_t launch_moe_skinny(const MxMoeArgs &a, int max_tiles, hipStream_t st)
@@ -229,7 +259,7 @@ hipError_t launch_moe_skinny(const MxMoeArgs &a, int max_tiles, hipStream_t st)
     p.ytype = a.type;
     p.M = (int)a.I;
     p.K = (int)a.H;
-    hipError_t err = launch_expert<kGateUp>(p, a.type == kBF16, a.T * a.topk, st);
+    hipError_t err = launch_expert<kGateUp>(p, a.type == kBF16, st);
     if (err != hipSuccess)
         return err;
     p.w = a.down;
@@ -238,7 +268,7 @@ hipError_t launch_moe_skinny(const MxMoeArgs &a, int max_tiles, hipStream_t st)
     p.ytype = kF32;
     p.M = (int)a.H;
     p.K = (int)a.I;
-    return launch_expert<kDown>(p, a.type == kBF16, a.T * a.topk, st);
+    return launch_expert<kDown>(p, a.type == kBF16, st);
 }
 
 } // namespace
