@@ -16,12 +16,34 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p)
     return (uint32_t)(size_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-// The tile of this workgroup in XCD-contiguous order, -1 past the last.
-__device__ __forceinline__ int xcd_tile(int total)
+// The work of this workgroup.  Workgroups are dealt to the 8 XCDs in turn; each XCD gets a
+// contiguous run of tiles.  Where the last round of tiles would leave at least half the CUs
+// idle, its tiles are cut in two along the activation rows: `whole` tiles come first, the
+// rest as halves (14336 x 4096 by 4096 rows is 3.5 rounds of 256 x 256 tiles on 256 CUs).
+struct TileWork {
+    int tile, half; // half: -1 whole, else 0 or 1; tile -1: nothing
+};
+__device__ __forceinline__ TileWork tile_work(int total, int whole)
 {
-    const int b = blockIdx.x, per = (total + 7) / 8;
-    const int t = (b % 8) * per + b / 8;
-    return t < total ? t : -1;
+    int b = blockIdx.x;
+    const bool cut = b >= (whole + 7) / 8 * 8;
+    const int n = cut ? 2 * (total - whole) : whole;
+    if (cut)
+        b -= (whole + 7) / 8 * 8;
+    const int t = (b % 8) * ((n + 7) / 8) + b / 8;
+    if (t >= n)
+        return {-1, -1};
+    return cut ? TileWork{whole + t / 2, t & 1} : TileWork{t, -1};
+}
+// How many of the tiles are not cut, and the workgroups of the launch.
+inline int tiles_whole(int64_t total, int64_t cus)
+{
+    const int64_t rest = total % cus;
+    return (int)(rest > 0 && 2 * rest <= cus ? total - rest : total);
+}
+inline unsigned tile_grid(int64_t total, int64_t whole)
+{
+    return (unsigned)((whole + 7) / 8 * 8 + (2 * (total - whole) + 7) / 8 * 8);
 }
 
 // The run of K of one of KG groups of waves, in blocks of 32 columns: of the whole

@@ -42,7 +42,7 @@ struct TileArgs {
     void *y;
     int ytype;
     int M, K, N;
-    int tiles_m, tiles_total;
+    int tiles_m, tiles_total, tiles_whole;
 };
 
 template <int OA, int OB>
@@ -58,21 +58,21 @@ __device__ __forceinline__ float16_t mx_mfma32_fp4(uint4 a, uint32_t sa, uint4 b
 // SL: the scales go through LDS as well (K % 512 == 0, so that sixteen scales of a
 // row, two stages', are one aligned copy); otherwise registers.
 template <int WM, int WN, int FM, int FN, bool SL>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(TileArgs p)
+constexpr int mx_lds_bytes()
+{
+    constexpr int BR = 32 * FM * WM + 32 * FN * WN;
+    return std::max(2 * BR * 128 + (SL ? 2 * BR * 16 : 0), WM * WN * store_scratch(4 * FM, 4));
+}
+
+// The tile of weight rows m0 .. and activation rows n0 ..
+template <int WM, int WN, int FM, int FN, bool SL>
+__device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8_t *lds)
 {
     constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN, BR = BM + BN;
     constexpr int NC = BR / 8 / NW;                      // 1 KB copies per wave and stage
     constexpr int NS = SL ? (BR / 64 + NW - 1) / NW : 0; // 64-row scale copies
     constexpr int kScales = 2 * BR * 128;                // byte offset of the scales
     static_assert(NC * 8 * NW == BR && BM % 64 == 0 && BN % 64 == 0, "whole copies");
-    __shared__ __attribute__((aligned(16))) uint8_t
-        lds[std::max(2 * BR * 128 + (SL ? 2 * BR * 16 : 0), NW * store_scratch(4 * FM, 4))];
-    const int tile = xcd_tile(p.tiles_total);
-    if (tile < 0)
-        return;
-    int tm, tn;
-    tile_pos(tile, p.tiles_m, p.tiles_total / p.tiles_m, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
     const int M = p.M, K = p.K;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -285,13 +285,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(TileArgs p)
     }
 }
 
+// Whether a launch of these tiles may cut its last ones: the 256-row ones (14336 x 4096 by
+// 4096 rows, 3.5 rounds, 133 -> 130.5 us; smaller tiles won nothing).
+constexpr bool cuts(int FM) { return FM == 4; }
+
+template <int WM, int WN, int FM, int FN, bool SL>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(TileArgs p)
+{
+    constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[mx_lds_bytes<WM, WN, FM, FN, SL>()];
+    const TileWork work = tile_work(p.tiles_total, p.tiles_whole);
+    if (work.tile < 0)
+        return;
+    int tm, tn;
+    tile_pos(work.tile, p.tiles_m, p.tiles_total / p.tiles_m, tm, tn);
+    if constexpr (cuts(FM)) {
+        if (work.half >= 0) {
+            const int n0 = tn * BN + work.half * (BN / 2);
+            if (n0 < p.N)
+                mx_tile<WM, WN, FM, FN / 2, SL>(p, tm * BM, n0, lds);
+            return;
+        }
+    }
+    mx_tile<WM, WN, FM, FN, SL>(p, tm * BM, tn * BN, lds);
+}
+
 template <int WM, int WN, int FM, int FN>
 hipError_t launch_mx(TileArgs p, hipStream_t st)
 {
     constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
     p.tiles_m = (p.M + BM - 1) / BM;
     p.tiles_total = p.tiles_m * ((p.N + BN - 1) / BN);
-    const dim3 grid((unsigned)((p.tiles_total + 7) / 8 * 8)), block(64 * WM * WN);
+    p.tiles_whole = cuts(FM) ? tiles_whole(p.tiles_total, device_cus()) : p.tiles_total;
+    const dim3 grid(tile_grid(p.tiles_total, p.tiles_whole)), block(64 * WM * WN);
     if (p.K % 512 == 0)
         hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FM, FN, true>), grid, block, 0, st, p);
     else

@@ -209,7 +209,7 @@ def test_gemv_wide_range_activations(B):
                                    (4100, 1024, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
                                    (14300, 96, 1030), (4096, 4096, 130), (4100, 1152, 130),
                                    (4100, 2080, 130), (1000, 768, 40), (1000, 800, 40),
-                                   (1000, 1024, 40), (100, 992, 200), (70, 256, 20), (70, 2048, 20)])
+                                   (16500, 640, 1030), (1000, 1024, 40), (100, 992, 200), (70, 256, 20), (70, 2048, 20)])
 def test_gemm(M, K, N, t):
     q, s, W = weights(10, M, K)
     xd, x64 = as_type(normal(11, N, K), t)
@@ -225,7 +225,7 @@ def test_gemm(M, K, N, t):
                                    (128, 14336, 7), (515, 288, 300), (1024, 1024, 512),
                                    # each tile size, with and without whole 512-column chunks
                                    (4100, 512, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
-                                   (14300, 96, 1030)])
+                                   (14300, 96, 1030), (16500, 640, 1100)])
 def test_mxgemm(M, K, N, t):
     torch = torch_cuda()
     q, s, W = weights(12, M, K)
