@@ -123,7 +123,7 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
         const int idx = CX * wave + i;
         const int src = min(st, nst - 1);
         const uint32_t last = (uint32_t)(4 * (nblk - 2 * src) - 1); // chunks past it repeat it
-        load_lds16(xb + (int64_t)src * 64, xoff[i] + 16u * min(xchk[i], last),
+        load_lds16(xb + (int64_t)src * 64, xoff[i] + 16u * (SM == kScale1 ? min(xchk[i], last) : xchk[i]),
                    __builtin_amdgcn_readfirstlane(base + st % NB * (BN * 128) + 1024u * idx));
     };
     auto copy_w1 = [&](int q, int i) { // quarter q & 3 of chunk q >> 2
@@ -133,8 +133,9 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
         const int row0 = 8 * (BM / 32 * (q & 3) + idx), row = row0 + (lane >> 3);
         const bool second = MODE == kGateUp && row0 >= BW;
         const int rr = min(second ? row - BW : row, mv - 1);
+        const uint32_t chk = (uint32_t)((lane & 7) ^ swz8(row));
         load_lds16((second ? wq1 : wq0) + (int64_t)src * 128,
-                   (uint32_t)rr * (uint32_t)(K >> 1) + 16u * min((uint32_t)((lane & 7) ^ swz8(row)), last),
+                   (uint32_t)rr * (uint32_t)(K >> 1) + 16u * (SM == kScale16 ? chk : min(chk, last)),
                    __builtin_amdgcn_readfirstlane(base + kW + ch % NC * (BM * 128) + 128u * row0));
     };
     auto copy_s = [&](int c) { // 512-column chunk c
@@ -214,13 +215,12 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             acc[i][j] = float16_t{};
-    auto multiply = [&](bool live, uint4 (&a)[FM], uint4 (&b)[FN], auto between) {
+    auto multiply = [&](uint4 (&a)[FM], uint4 (&b)[FN], auto between) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                if (live)
-                    acc[i][j] = mfma32<BF16>(a[i], b[j], acc[i][j]);
+                acc[i][j] = mfma32<BF16>(a[i], b[j], acc[i][j]);
                 // the products stay where they are written, between reads and copies
                 if constexpr (AGPR)
                     asm volatile("" : "+a"(acc[i][j]));
@@ -294,34 +294,41 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
                 read_x(st, s, o.b[s]);
         };
         auto stage = [&](int st, Ops &cur, Ops &nxt) {
-            const bool live = KG == 1 || st < nst; // (a shorter run idles at the end)
             // the next stage's copies have landed, every wave has read this one's
             wait_copies<(NB - 2) * (CX + CW)>();
             load(st + 1, nxt); // (after the last stage: read and not used)
-            uint4 a[FM];
-            convert(cur.c, I0{}, a);
+            uint4 a0[FM], a1[FM];
+            // one copy after each of the first products
+            constexpr int P = FM * FN;
+            auto copies = [&](int s) {
+                return [&, s](int u) { group(st + NB, s * P + u); };
+            };
+            convert(cur.c, I0{}, a0);
+            convert(cur.c, I1{}, a1);
             mask_x(st, cur.b[0]);
-            multiply(live, a, cur.b[0], [&](int u) { group(st + NB, u); });
-#pragma unroll
-            for (int u = FM * FN; u < CX + CW + 1; ++u)
-                group(st + NB, u);
-            convert(cur.c, I1{}, a);
+            multiply(a0, cur.b[0], copies(0));
+            convert(cur.c, I2{}, a0);
             mask_x(st, cur.b[1]);
-            multiply(live, a, cur.b[1], nothing);
-            convert(cur.c, I2{}, a);
+            multiply(a1, cur.b[1], copies(1));
+            convert(cur.c, I3{}, a1);
             mask_x(st, cur.b[2]);
-            multiply(live, a, cur.b[2], nothing);
-            convert(cur.c, I3{}, a);
+            multiply(a0, cur.b[2], copies(2));
             mask_x(st, cur.b[3]);
-            multiply(live, a, cur.b[3], nothing);
+            multiply(a1, cur.b[3], copies(3));
+#pragma unroll
+            for (int u = 4 * P; u < CX + CW + 1; ++u)
+                group(st + NB, u);
         };
         Ops o0, o1;
         load(0, o0);
-        for (int st = 0; st < steps; st += 2) {
+        for (int st = 0; st < nst; st += 2) {
             stage(st, o0, o1);
-            if (st + 1 < steps)
+            if (st + 1 < nst)
                 stage(st + 1, o1, o0);
         }
+        if constexpr (KG > 1) // a shorter run keeps the others' barriers
+            for (int st = nst; st < steps; ++st)
+                wait_copies<0>();
     } else {
         Codes c0, c1;
         uint4 a0[FM], a1[FM], b0[FN], b1[FN];
@@ -329,20 +336,20 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
         read_x(0, 0, b0);
         mask_x(0, b0);
         convert(c0, I0{}, a0);
-        for (int st = 0; st < steps; ++st) {
-            const bool live = KG == 1 || st < nst; // (a shorter run idles at the end)
+        static_assert(KG == 1, "one run");
+        for (int st = 0; st < nst; ++st) {
             read_x(st, 1, b1);
             read_codes(st + 1, c1); // (after the last stage: read and not used)
             convert(c0, I1{}, a1);
-            multiply(live, a0, b0, nothing);
+            multiply(a0, b0, nothing);
             read_x(st, 2, b0);
             mask_x(st, b1);
             convert(c0, I2{}, a0);
-            multiply(live, a1, b1, nothing);
+            multiply(a1, b1, nothing);
             read_x(st, 3, b1);
             mask_x(st, b0);
             convert(c0, I3{}, a1);
-            multiply(live, a0, b0, nothing);
+            multiply(a0, b0, nothing);
             // the next stage's copies have landed and every wave has read this stage,
             // whose place the one after takes
             wait_copies<(NB - 2) * (CX + CW)>();
@@ -350,7 +357,7 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
             mask_x(st, b1);
             c0 = c1;
             convert(c0, I0{}, a0);
-            multiply(live, a1, b1, [&](int u) { group(st + NB, u); });
+            multiply(a1, b1, [&](int u) { group(st + NB, u); });
 #pragma unroll
             for (int u = FM * FN; u < CX + CW + 1; ++u)
                 group(st + NB, u);
