@@ -440,7 +440,9 @@ template <bool BF16, int WM, int WN, int KG, int FM, int FN, int NB, int SM>
 __global__ __launch_bounds__(64 * WM * WN * KG, 2) void gemm_tile16_kernel(Tile16Args p)
 {
     constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[KG * lds_bytes(BM, BN, NB, SM)];
+    // (halves have room for another stage)
+    constexpr int kBytes = KG * lds_bytes(BM, BN, NB, SM), kHalf = lds_bytes(BM, BN / 2, NB + 1, SM);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[cuts(FN) && kHalf > kBytes ? kHalf : kBytes];
     const TileWork work = tile_work(p.tiles_total, p.tiles_whole);
     if (work.tile < 0)
         return;
@@ -450,8 +452,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void gemm_tile16_kernel(Tile1
         if (work.half >= 0) {
             const int n0 = tn * BN + work.half * (BN / 2);
             if (n0 < p.N)
-                tile16<BF16, kDense, WM, WN, KG, FM, FN / 2, NB, SM>(p, tm * BM, n0, min(p.N - n0, BN / 2),
-                                                                     0, lds);
+                tile16<BF16, kDense, WM, WN, KG, FM, FN / 2, NB + 1, SM>(p, tm * BM, n0,
+                                                                         min(p.N - n0, BN / 2), 0, lds);
             return;
         }
     }
@@ -542,27 +544,34 @@ hipError_t launch_moe_pair(const MxMoeArgs &a, int max_tiles, hipStream_t st)
     return launch_moe_one<BF16, kDown, WM, WN, KG, FM, FN, FR, NB>(p, st);
 }
 
-// The tile for a shape, from an estimate of its time in us per 1024 columns: rounds of
-// tiles on the device times a round's time, with a lone tile's as the floor.  Measured
-// (K 4096 and 14336): 256 x 256 tiles 17 alone, 24 a full round; 128 x 128 9.3 alone, 10
-// at one per CU, 15-16 at two, 29 at four; 64 x 64 with K in two runs 4.0, 4.6, 5.4-6.2,
-// 11-12; in four runs 3.2, 3.4-3.9, 7-8; 64 x 32 in four runs 2.4-2.9, 3.3, 5.8.  So
-// 4096 x 14336 takes by 64 rows 33 us on 64 x 32 tiles (48, 68 on the next), by 130 rows
-// 47 on 64 x 64 in four runs (62, 66), by 512 rows 75 in two runs (98, 129), by 1024 rows
-// 142 on 128 x 128 (150, 234); 14336 x 4096 by 1024 rows 97 on 256 x 256 (115, 160).
+// The tile for a shape, from an estimate of its time in us per 1024 columns: full rounds of
+// tiles on the device at `full`, a last one between `lone` and `full` by how many CUs it
+// has.  All but the 256 x 256 tiles, whose LDS holds no more, keep two or more stages of
+// copies in flight: one stage in flight leaves every stage the length of a read from
+// memory.  Measured with the weights coming from HBM, one workgroup a CU, us for K 14336
+// alone and full: 256 x 256 214, 350; 256 x 128 169, 188; 128 x 128 106, 115 (one stage in
+// flight 165, and 197 for two a CU); 128 x 64 with K in two runs 61, 68 (72); 64 x 64 in two
+// runs 40, 44 (one stage, four runs 53, 57); 64 x 32 in four runs 30, 28.  So 4096 x 14336
+// takes by 64 rows 31 us on 64 x 32 tiles (43, 62 on the next), by 130 rows 40 on 64 x 64
+// (53, 61), by 512 rows 68 on 128 x 64 (85, 106), by 1024 rows 115 on 128 x 128 (129, 169),
+// by 2048 rows 188 on 256 x 128 (219, 228); 14336 x 4096 by 1024 rows 95 on 256 x 256 (109).
 int tile16_choice(int64_t M, int64_t K, int64_t N)
 {
     const int64_t cus = device_cus(), chunks = (K + 255) / 256;
-    auto rounds = [&](int64_t bm, int64_t bn) {
-        return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + cus - 1) / cus);
+    auto time = [&](int64_t bm, int64_t bn, double lone, double full) {
+        const int64_t tiles = (M + bm - 1) / bm * ((N + bn - 1) / bn), rest = tiles % cus;
+        return (double)(tiles / cus) * full + (rest ? lone + (full - lone) * rest / cus : 0);
     };
-    const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
-    const double half = tiles_whole(big, cus) < big ? 0.4 : 0; // saved in a round of halves
-    const double t[5] = {24.0 * (rounds(256, 256) - half), std::max(9.5, 7.7 * rounds(128, 128)),
-                         chunks >= 2 ? std::max(4.2, 2.9 * rounds(64, 64)) : 1e30,
-                         chunks >= 4 ? 3.5 * rounds(64, 64) : 1e30,
-                         chunks >= 4 ? 2.8 * rounds(64, 32) : 1e30};
-    return (int)(std::min_element(t, t + 5) - t);
+    // 256 x 256: a last round cut in halves costs about what one of 256 x 128 does
+    const int64_t big = (M + 255) / 256 * ((N + 255) / 256), whole = tiles_whole(big, cus);
+    const double cut = whole < big ? 12.6 + 1.8 * 2 * (double)(big - whole) / cus : 0;
+    const double t[6] = {whole < big ? 24.0 * (double)(whole / cus) + cut : time(256, 256, 15.3, 24.0),
+                         time(256, 128, 12.1, 13.5),
+                         time(128, 128, 7.6, 8.3),
+                         chunks >= 2 ? time(128, 64, 4.35, 4.9) : 1e30,
+                         chunks >= 2 ? time(64, 64, 2.9, 3.1) : 1e30,
+                         chunks >= 4 ? time(64, 32, 2.15, 2.0) : 1e30};
+    return (int)(std::min_element(t, t + 6) - t);
 }
 
 template <bool BF16, int WM, int WN, int KG, int FM, int FN, int NB>
@@ -593,9 +602,10 @@ hipError_t launch_dense_choice(const Tile16Args &p, hipStream_t st)
 {
     switch (tile16_choice(p.M, p.K, p.N)) {
     case 0: return launch_dense<BF16, 4, 2, 1, 2, 4, 2>(p, st);
-    case 1: return launch_dense<BF16, 2, 2, 1, 2, 2, 2>(p, st);
-    case 2: return launch_dense<BF16, 2, 1, 2, 1, 2, 2>(p, st);
-    case 3: return launch_dense<BF16, 2, 1, 4, 1, 2, 2>(p, st);
+    case 1: return launch_dense<BF16, 2, 2, 1, 4, 2, 2>(p, st);
+    case 2: return launch_dense<BF16, 2, 2, 1, 2, 2, 3>(p, st);
+    case 3: return launch_dense<BF16, 2, 1, 2, 2, 2, 3>(p, st);
+    case 4: return launch_dense<BF16, 2, 1, 2, 1, 2, 4>(p, st);
     default: return launch_dense<BF16, 2, 1, 4, 1, 1, 3>(p, st);
     }
 }
