@@ -4,17 +4,17 @@
 // weight rows by 32 FN WN activation rows; a wave holds FM x FN accumulators of the
 // scaled 32x32x64 product, whose operand is one block (16 bytes, one scale) per lane
 // as it lies in memory.  Codes go global -> LDS by direct copies, 256 columns (128
-// bytes of a row: whole cache lines) per stage, two stages in turn; the scales go
+// bytes of a row: whole cache lines) per stage, NB stages in turn; the scales go
 // along, 16 bytes of a row (512 columns) every second stage, since a line fetched per
 // row and stage for four or eight bytes of scales would cost as much as the codes.
 //
 // What bounds it, on 256 x 256 tiles at 4096 x 14336 by 4096 rows: the matrix cores
-// under the power limit.  The kernel takes 113 us (4.2 PFLOP/s); with the copies and
-// the LDS reads taken out, the same products on unchanging registers take 94 us,
-// without the copies 104, without the reads 113 us.  Steps that got there (same
-// shape): stages of 128 columns with the scales by dwords 152 us (bound by requests
-// to the L2), 128-byte rows and 16-byte scales 130, operands read a step ahead with
-// the products pinned between the reads 117, copies spread between the products 113.
+// under the power limit.  The kernel takes 109 us (4.4 PFLOP/s); the same products on
+// unchanging registers, without copies and LDS reads, take 94 us.  Steps that got there
+// (same shape): stages of 128 columns with the scales by dwords 152 us (bound by requests
+// to the L2), 128-byte rows and 16-byte scales 130, operands read a step ahead with the
+// products pinned between the reads 117, copies spread between the products 113, results
+// stored through LDS 109.
 //
 // LDS rows are 128 bytes (eight blocks); block c of row r sits in slot
 // c ^ ((r >> 1) & 7): the 16 lanes of a read phase touch 16 rows and 16 distinct
@@ -57,21 +57,25 @@ __device__ __forceinline__ float16_t mx_mfma32_fp4(uint4 a, uint32_t sa, uint4 b
 
 // SL: the scales go through LDS as well (K % 512 == 0, so that sixteen scales of a
 // row, two stages', are one aligned copy); otherwise registers.
-template <int WM, int WN, int FM, int FN, bool SL>
+template <int WM, int WN, int FM, int FN, int NB, bool SL>
 constexpr int mx_lds_bytes()
 {
     constexpr int BR = 32 * FM * WM + 32 * FN * WN;
-    return std::max(2 * BR * 128 + (SL ? 2 * BR * 16 : 0), WM * WN * store_scratch(4 * FM, 4));
+    return std::max(NB * BR * 128 + (SL ? (NB / 2 + 1) * BR * 16 : 0), WM * WN * store_scratch(4 * FM, 4));
 }
 
-// The tile of weight rows m0 .. and activation rows n0 ..
-template <int WM, int WN, int FM, int FN, bool SL>
+// The tile of weight rows m0 .. and activation rows n0 ..: NB stages in LDS, of which
+// NB - 1 are in flight when a stage begins.
+template <int WM, int WN, int FM, int FN, int NB, bool SL>
 __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8_t *lds)
 {
     constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN, BR = BM + BN;
     constexpr int NC = BR / 8 / NW;                      // 1 KB copies per wave and stage
     constexpr int NS = SL ? (BR / 64 + NW - 1) / NW : 0; // 64-row scale copies
-    constexpr int kScales = 2 * BR * 128;                // byte offset of the scales
+    constexpr int kScales = NB * BR * 128;               // byte offset of the scales
+    constexpr int NSB = NB / 2 + 1;                      // and their 512-column places
+    // one wave a SIMD: the compiler keeps the accumulators in the other register file
+    constexpr bool AGPR = NW <= 4 && mx_lds_bytes<WM, WN, FM, FN, NB, SL>() > (80 << 10);
     static_assert(NC * 8 * NW == BR && BM % 64 == 0 && BN % 64 == 0, "whole copies");
     const int M = p.M, K = p.K;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -111,12 +115,12 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
             const int row0 = 8 * (NC * wave + i);
             load_lds16((row0 < BM ? aq : bq) + (int64_t)src * 128,
                        off[i] + 16u * (SL ? chk[i] : min(chk[i], last)),
-                       __builtin_amdgcn_readfirstlane(base + ((st & 1) * BR + row0) * 128));
+                       __builtin_amdgcn_readfirstlane(base + (st % NB * BR + row0) * 128));
         } else if (i < NC + NS && (st & 1) == 0) {
             const int row0 = min(64 * (NS * wave + i - NC), BR - 64);
             load_lds16((row0 < BM ? as : bs) + (int64_t)(src >> 1) * 16, soff[i - NC],
                        __builtin_amdgcn_readfirstlane(base + kScales +
-                                                      ((st >> 1 & 1) * BR + row0) * 16));
+                                                      ((st >> 1) % NSB * BR + row0) * 16));
         }
     };
 
@@ -150,7 +154,7 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
         return v;
     };
     auto scales = [&](int st, Scale &s) {
-        const uint8_t *S = lds + kScales + (st >> 1 & 1) * BR * 16 + 8 * (st & 1);
+        const uint8_t *S = lds + kScales + (st >> 1) % NSB * BR * 16 + 8 * (st & 1);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int row = 32 * (FM * wm + i) + r;
@@ -183,7 +187,7 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
         rof[t] = r * 128 + 16 * ((2 * t + h) ^ swz8(r));
     const int arow = 32 * FM * wm * 128, brow = (BM + 32 * FN * wn) * 128;
     auto read = [&](int st, int t, Frag &f) {
-        const uint8_t *S = lds + (st & 1) * BR * 128 + rof[t];
+        const uint8_t *S = lds + st % NB * BR * 128 + rof[t];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
             f.a[i] = ld16(S + arow + 32 * i * 128);
@@ -215,7 +219,10 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
                     f.a[i], t < 2 ? s.a[i].x : s.a[i].y, f.b[j], t < 2 ? s.b[j].x : s.b[j].y,
                     acc[i][j]);
                 // the products stay where they are written, between reads and copies
-                asm volatile("" : "+v"(acc[i][j]));
+                if constexpr (AGPR)
+                    asm volatile("" : "+a"(acc[i][j]));
+                else
+                    asm volatile("" : "+v"(acc[i][j]));
                 const int u = i * FN + j;
                 if (c0 >= 0 && u % EV == EV - 1 && u / EV < CP && c0 + u / EV < NC + NS)
                     copy1(stc, c0 + u / EV);
@@ -231,30 +238,32 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
     // the matrix cores do.
     constexpr int CP = (NC + NS + 1) / 2;
 #pragma unroll
-    for (int i = 0; i < NC + NS; ++i)
-        copy1(0, i);
-    wait_copies<0>();
+    for (int g = 0; g < NB - 1; ++g)
+#pragma unroll
+        for (int i = 0; i < NC + NS; ++i)
+            copy1(g, i);
+    wait_copies<(NB - 2) * NC>(); // (scale copies among the newer ones: a wait for more)
     Frag f0, f1;
     Scale s0, s1;
     scales(0, s0);
     read(0, 0, f0);
 #pragma unroll
     for (int i = 0; i < CP; ++i)
-        copy1(1, i);
+        copy1(NB - 1, i);
     for (int st = 0; st < nst; ++st) {
         shift(s0);
         read(st, 1, f1);
-        multiply(st, std::integral_constant<int, 0>{}, f0, s0, st + 1, CP);
+        multiply(st, std::integral_constant<int, 0>{}, f0, s0, st + NB - 1, CP);
         read(st, 2, f0);
         multiply(st, std::integral_constant<int, 1>{}, f1, s0, 0, -1);
         read(st, 3, f1);
         multiply(st, std::integral_constant<int, 2>{}, f0, s0, 0, -1);
         // the next stage's copies have landed and every wave has read this stage,
         // whose place the one after takes
-        wait_copies<0>();
+        wait_copies<(NB - 2) * NC>();
         scales(st + 1, s1); // (after the last stage: read and not used)
         read(st + 1, 0, f0);
-        multiply(st, std::integral_constant<int, 3>{}, f1, s0, st + 2, 0);
+        multiply(st, std::integral_constant<int, 3>{}, f1, s0, st + NB, 0);
         s0 = s1;
     }
     wait_copies<0>();
@@ -286,14 +295,16 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
 }
 
 // Whether a launch of these tiles may cut its last ones: the 256-row ones (14336 x 4096 by
-// 4096 rows, 3.5 rounds, 133 -> 130.5 us; smaller tiles won nothing).
+// 4096 rows, 3.5 rounds, 133 -> 126 us; smaller tiles won nothing).
 constexpr bool cuts(int FM) { return FM == 4; }
 
-template <int WM, int WN, int FM, int FN, bool SL>
+template <int WM, int WN, int FM, int FN, int NB, bool SL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(TileArgs p)
 {
     constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[mx_lds_bytes<WM, WN, FM, FN, SL>()];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(
+        mx_lds_bytes<WM, WN, FM, FN, NB, SL>(),
+        cuts(FM) ? mx_lds_bytes<WM, WN, FM, FN / 2, NB + 1, SL>() : 0)]; // (halves: one stage more)
     const TileWork work = tile_work(p.tiles_total, p.tiles_whole);
     if (work.tile < 0)
         return;
@@ -303,14 +314,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx_tile_kernel(TileArgs p)
         if (work.half >= 0) {
             const int n0 = tn * BN + work.half * (BN / 2);
             if (n0 < p.N)
-                mx_tile<WM, WN, FM, FN / 2, SL>(p, tm * BM, n0, lds);
+                mx_tile<WM, WN, FM, FN / 2, NB + 1, SL>(p, tm * BM, n0, lds);
             return;
         }
     }
-    mx_tile<WM, WN, FM, FN, SL>(p, tm * BM, tn * BN, lds);
+    mx_tile<WM, WN, FM, FN, NB, SL>(p, tm * BM, tn * BN, lds);
 }
 
-template <int WM, int WN, int FM, int FN>
+template <int WM, int WN, int FM, int FN, int NB>
 hipError_t launch_mx(TileArgs p, hipStream_t st)
 {
     constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
@@ -319,30 +330,35 @@ hipError_t launch_mx(TileArgs p, hipStream_t st)
     p.tiles_whole = cuts(FM) ? tiles_whole(p.tiles_total, device_cus()) : p.tiles_total;
     const dim3 grid(tile_grid(p.tiles_total, p.tiles_whole)), block(64 * WM * WN);
     if (p.K % 512 == 0)
-        hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FM, FN, true>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FM, FN, NB, true>), grid, block, 0, st, p);
     else
-        hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FM, FN, false>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((mx_tile_kernel<WM, WN, FM, FN, NB, false>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 
 } // namespace
 
-// The tile for a shape, from an estimate of the time of a stage (256 columns):
-// rounds of tiles on the device times what a round takes, with what a lone tile takes
-// as the floor.  Measured, us per stage, K 4096 and 14336: 64 x 64 tiles 0.53 alone,
-// 0.65 at two per CU, 1.1 at four, 2.3 at seven; 128 x 128 0.8 alone, 0.9 at one per CU,
-// 1.6 at two, 2.5-3.0 at four; 256 x 256 2.1-2.4 per round.  So 4096 x 4096 by 512 rows
-// takes 12 us on the first (14 on the second), 4096 x 14336 by 1024 rows 51 us on the
-// second (62, 80 on the others), 14336 x 4096 by 1024 rows 40 us on the third (48).
+// The tile for a shape, from an estimate of the time of a stage (256 columns): full rounds
+// of tiles on the device, and a last one by how many CUs it has.  The smaller tiles keep
+// two or three stages of copies in flight: with one, a stage of a lone tile takes the
+// length of a read from memory.  Measured with the weights coming from HBM, us for K 14336
+// (56 stages): 64 x 64 tiles 22 up to one per CU (one stage in flight 44), 41 at two, 71 at
+// four; 128 x 128 35 alone, 45 at one per CU (one stage in flight 53, 58), 79 at two;
+// 256 x 256 59-70 for a round in halves, 85 alone, 110-120 a full round.  So 4096 x 14336
+// takes by 130 rows 22 us on the first (36, 59 on the others), by 1024 rows 45 on the second
+// (71, 66), by 2048 rows 70 on the third (127, 79).
 static int mx_tile_choice(int64_t M, int64_t N)
 {
     const int64_t cus = device_cus();
-    auto rounds = [&](int64_t b) {
-        const int64_t tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
-        return (double)((tiles + cus - 1) / cus);
+    auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b); };
+    auto last = [&](int64_t rest, double lone, double full) {
+        return rest ? lone + (full - lone) * (double)rest / (double)cus : 0;
     };
-    const double t64 = std::max(0.55, 0.3 * rounds(64)), t128 = std::max(0.8, 0.75 * rounds(128));
-    const double t256 = 2.2 * rounds(256);
+    const int64_t t1 = tiles(64), t2 = tiles(128), t3 = tiles(256), whole = tiles_whole(t3, cus);
+    const double t64 = 0.39 + 0.36 * std::max(0.0, (double)t1 / (double)cus - 1.0);
+    const double t128 = 0.75 * (double)(t2 / cus) + last(t2 % cus, 0.63, 0.78);
+    const double t256 = 2.1 * (double)(t3 / cus) +
+                        (whole < t3 ? last(2 * (t3 - whole), 1.02, 1.22) : last(t3 % cus, 1.5, 2.1));
     return t64 <= t128 && t64 <= t256 ? 64 : t128 <= t256 ? 128 : 256;
 }
 
@@ -359,9 +375,9 @@ hipError_t launch_mx_tiles(MxMat w, MxMat x, void *y, int type, int64_t M, int64
     p.K = (int)K;
     p.N = (int)N;
     switch (mx_tile_choice(M, N)) {
-    case 64: return launch_mx<2, 2, 1, 1>(p, st);
-    case 128: return launch_mx<2, 2, 2, 2>(p, st);
-    default: return launch_mx<2, 4, 4, 2>(p, st);
+    case 64: return launch_mx<2, 2, 1, 1, 4>(p, st);
+    case 128: return launch_mx<2, 2, 2, 2, 3>(p, st);
+    default: return launch_mx<2, 4, 4, 2, 2>(p, st);
     }
 }
 

@@ -3,8 +3,8 @@
 //
 // A workgroup of WM x WN waves owns 32 FM WM weight rows by 32 FN WN activation rows;
 // a wave holds FM x FN accumulators of the 32x32x16 product.  Activations go global ->
-// LDS by direct copies, 64 columns (128 bytes of a row) per stage, two stages in turn.
-// Codes go the same way, 256 columns (128 bytes) per chunk, two chunks in turn, a
+// LDS by direct copies, 64 columns (128 bytes of a row) per stage, NB stages in turn.
+// Codes go the same way, 256 columns (128 bytes) per chunk, two or three in turn, a
 // quarter of a chunk's rows per stage; scales 512 columns (16 bytes) at a time.
 //
 // Lane (r, h) of a stage takes block h of weight row r: one 16-byte LDS read and one
@@ -249,7 +249,7 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
     using I3 = std::integral_constant<int, 3>;
 
     // Copies go in groups: group g is the activations of stage g, quarter g + 4 of the
-    // codes and, every eighth time, the scales stage g + 1 begins with.  After the
+    // codes (WIDE: g + 3) and, every eighth time, the scales stage g + 1 begins with.  After the
     // barrier that ends stage st (every wave has read stage st, and the codes of stage
     // st + 1) group st + NB takes the places that came free: activations of stage st,
     // codes of chunk (st + NB + 4) / 4 - NC, whose last stage is at most st + 1 while
@@ -432,8 +432,8 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
 }
 
 // Whether a launch of these tiles may cut its last ones: the 256-row ones.  14336 x 4096 by
-// 4096 rows (3.5 rounds) 375 -> 367 us, by 300 rows 63 -> 54.6; 128-row tiles lost 2-4 % to
-// the second body at most shapes (5120 x 5120 by 2048 rows gained 7 %).
+// 4096 rows (3.5 rounds) 375 -> 356 us; 128-row tiles lost 2-4 % to the second body at
+// most shapes.
 constexpr bool cuts(int FN) { return FN == 4; }
 
 template <bool BF16, int WM, int WN, int KG, int FM, int FN, int NB, int SM>
