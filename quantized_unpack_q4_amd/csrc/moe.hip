@@ -14,6 +14,7 @@
 //               the 256 x 256 tiles of gemm_big.hip from 160 on);
 //   3. down     grouped matrix product into binary32 rows (likewise);
 //   4. combine  out[t] = sum over slots, in slot order, of weight * row.
+// The layer over MXFP4 stacks (mxfp4_skinny.hip, mxfp4_tiles16.hip) shares 1 and 4.
 // No atomics touch the outputs and nothing waits on the host.
 #include "gq_device.h"
 #include "gq_internal.h"
@@ -220,16 +221,31 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restric
     if (c >= H)
         return;
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int s = 0; s < topk; ++s) {
-        const int pos = pos_of[(int64_t)t * topk + s];
-        if (pos < 0)
-            continue;
-        const float wgt = unit ? 1.f : wts[(int64_t)t * topk + s];
-        const float4 d = ldf4(D + (int64_t)pos * H + c);
-        a0 = fmaf(wgt, d.x, a0);
-        a1 = fmaf(wgt, d.y, a1);
-        a2 = fmaf(wgt, d.z, a2);
-        a3 = fmaf(wgt, d.w, a3);
+    // the rows of up to eight slots are loaded at once and added in slot order (top-8,
+    // hidden 2048: 4 tokens 4.4 -> 3.8 us, 2048 tokens 23 -> 21.9)
+    for (int s0 = 0; s0 < topk; s0 += 8) {
+        int pos[8];
+        float wgt[8];
+        float4 d[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) { // past the last slot: that one again, not added
+            const int64_t i = (int64_t)t * topk + min(s0 + u, topk - 1);
+            pos[u] = pos_of[i];
+            wgt[u] = wts[i];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) // (a dropped slot: any row, not added)
+            d[u] = ldf4(D + (int64_t)max(pos[u], 0) * H + c);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (s0 + u >= topk || pos[u] < 0)
+                continue;
+            const float w = unit ? 1.f : wgt[u];
+            a0 = fmaf(w, d[u].x, a0);
+            a1 = fmaf(w, d[u].y, a1);
+            a2 = fmaf(w, d[u].z, a2);
+            a3 = fmaf(w, d[u].w, a3);
+        }
     }
     *reinterpret_cast<uint2 *>(out + (int64_t)t * H + c) =
         make_uint2(mx_pack2<BF16>(a0, a1), mx_pack2<BF16>(a2, a3));

@@ -66,8 +66,7 @@ constexpr int lds_bytes(int BM, int BN, int NB, int SM)
 }
 
 // One tile: weight rows from m0 (gate/up: BM / 2 rows of each matrix) of expert e
-// against activation rows n0 .. n0 + nv - 1.  SL: the scales go through LDS
-// (K % 512 == 0), otherwise byte loads.
+// against activation rows n0 .. n0 + nv - 1.
 template <bool BF16, int MODE, int WM, int WN, int KG, int FM, int FN, int NB, int SM>
 __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int nv, int e,
                                        uint8_t *lds)

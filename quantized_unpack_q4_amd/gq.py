@@ -36,7 +36,8 @@ EXPORTS = (
     "gq_gemm_q4k_q8k",
     "gq_moe_workspace_bytes", "gq_moe_workspace_offsets", "gq_dequant_q8_0",
     "gq_dequant_q4k", "gq_quantize_mxfp4", "gq_dequant_mxfp4", "gq_gemv_mxfp4", "gq_gemm_mxfp4",
-    "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes", "gq_last_error", "gq_status_str", "gq_version",
+    "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes", "gq_last_error",
+    "gq_status_str", "gq_version",
 )
 
 
@@ -504,10 +505,8 @@ def quantize_q8k(x, stream=None):
 # microseconds on the device.
 
 _torch = None
-_mx_codes = {}
-
-
 _raw_stream = None
+_mx_codes = {}
 
 
 def _mx_enter(name, t):
