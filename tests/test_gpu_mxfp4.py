@@ -209,7 +209,12 @@ def test_gemv_wide_range_activations(B):
                                    (4100, 1024, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
                                    (14300, 96, 1030), (4096, 4096, 130), (4100, 1152, 130),
                                    (4100, 2080, 130), (1000, 768, 40), (1000, 800, 40),
-                                   (16500, 640, 1030), (1000, 1024, 40), (100, 992, 200), (70, 256, 20), (70, 2048, 20)])
+                                   (16500, 640, 1030), (1000, 1024, 40), (100, 992, 200),
+                                   # the same of the larger tiles, in whole rounds and halves
+                                   (16500, 96, 400), (16500, 96, 900), (6200, 640, 1300),
+                                   (6200, 512, 1300), (16500, 512, 900), (16500, 640, 200),
+                                   (16500, 512, 77), (16500, 288, 17), (16500, 512, 17),
+                                   (16500, 1024, 40), (8200, 1024, 40), (1000, 288, 17), (70, 256, 20), (70, 2048, 20)])
 def test_gemm(M, K, N, t):
     q, s, W = weights(10, M, K)
     xd, x64 = as_type(normal(11, N, K), t)
@@ -225,7 +230,9 @@ def test_gemm(M, K, N, t):
                                    (128, 14336, 7), (515, 288, 300), (1024, 1024, 512),
                                    # each tile size, with and without whole 512-column chunks
                                    (4100, 512, 1030), (4100, 1568, 1030), (14300, 1024, 1030),
-                                   (14300, 96, 1030), (16500, 640, 1100)])
+                                   (14300, 96, 1030), (16500, 640, 1100),
+                                   (16500, 96, 300), (16500, 512, 300), (8200, 2080, 77),
+                                   (8200, 1536, 77), (16500, 96, 400), (16500, 512, 400)])
 def test_mxgemm(M, K, N, t):
     torch = torch_cuda()
     q, s, W = weights(12, M, K)
@@ -504,6 +511,35 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in outs:
         assert torch.equal(a, b)
+
+
+def test_helpers_streams_shapes_and_no_rows():
+    torch = torch_cuda()
+    q, s, _ = weights(45, 40, 96)
+    x = torch.randn((5, 96), device="cuda")
+    want = gq.gemv_mxfp4(q, s, x)
+    # the default stream by its handle, one row without a rows' dimension, a batch of rows
+    assert torch.equal(gq.gemv_mxfp4(q, s, x, stream=0), want)
+    assert torch.equal(gq.gemv_mxfp4(q, s, x[2]), gq.gemv_mxfp4(q, s, x[2:3]))
+    a, b = gq.quantize_mxfp4(x)
+    for got, ref in ((gq.quantize_mxfp4(x[3]), (a[3], b[3])),
+                     (gq.quantize_mxfp4(x[:4].view(2, 2, 96)), (a[:4].view(2, 2, 48), b[:4].view(2, 2, 3)))):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    h = x.half()
+    y = gq.gemm_mxfp4(q, s, h)
+    assert torch.equal(gq.gemm_mxfp4(q, s, h.view(1, 5, 96)), y)
+    # no rows
+    none = torch.empty((0, 96), device="cuda")
+    nq, ns = gq.quantize_mxfp4(none)
+    assert nq.shape == (0, 48) and ns.shape == (0, 3)
+    assert gq.dequant_mxfp4(nq, ns).shape == (0, 96)
+    assert gq.gemv_mxfp4(q, s, none).shape == (0, 40)
+    assert gq.gemm_mxfp4(q, s, none.half()).shape == (0, 40)
+    assert gq.gemm_mxfp4_mxfp4(q, s, nq, ns).shape == (0, 40)
+    # a pointer that is not 16-byte aligned
+    with pytest.raises(gq.GQError) as e:
+        gq.gemv_mxfp4(q, s, torch.randn(97, device="cuda")[1:])
+    assert e.value.status == gq.GQ_EALIGN
 
 
 def test_helper_refusals():
