@@ -207,9 +207,41 @@ __global__ __launch_bounds__(kGroupThreads) void moe_group_kernel(
     }
 }
 
-// One thread per 4 output columns of one token; BF16: a bfloat16 output instead
-// of binary16.
-template <bool BF16>
+// Adds the rows of N slots of a token from slot s0 on, in slot order; the rows are loaded
+// at once.  Past the last slot that one is loaded again and not added.
+template <int N>
+__device__ __forceinline__ void combine_slots(const float *__restrict__ D,
+                                              const int32_t *__restrict__ pos_of,
+                                              const float *__restrict__ wts, int64_t first, int s0,
+                                              int topk, int H, int c, bool unit, float4_t &a)
+{
+    int pos[N];
+    float wgt[N];
+    float4 d[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int64_t i = first + min(s0 + u, topk - 1);
+        pos[u] = pos_of[i];
+        wgt[u] = wts[i];
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) // (a dropped slot: any row, not added)
+        d[u] = ldf4(D + (int64_t)max(pos[u], 0) * H + c);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (s0 + u >= topk || pos[u] < 0)
+            continue;
+        const float w = unit ? 1.f : wgt[u];
+        a[0] = fmaf(w, d[u].x, a[0]);
+        a[1] = fmaf(w, d[u].y, a[1]);
+        a[2] = fmaf(w, d[u].z, a[2]);
+        a[3] = fmaf(w, d[u].w, a[3]);
+    }
+}
+
+// One thread per 4 output columns of one token; BF16: a bfloat16 output instead of binary16.
+// The slots go N at a time (8: the rest as four, two or one).
+template <bool BF16, int N>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restrict__ D,
                                                           const int32_t *__restrict__ pos_of,
                                                           const float *__restrict__ wts,
@@ -220,35 +252,21 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float *__restric
     const int c = ((blockIdx.x % col_blocks) * 256 + threadIdx.x) * 4;
     if (c >= H)
         return;
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    // the rows of up to eight slots are loaded at once and added in slot order (top-8,
-    // hidden 2048: 4 tokens 4.4 -> 3.8 us, 2048 tokens 23 -> 21.9)
-    for (int s0 = 0; s0 < topk; s0 += 8) {
-        int pos[8];
-        float wgt[8];
-        float4 d[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) { // past the last slot: that one again, not added
-            const int64_t i = (int64_t)t * topk + min(s0 + u, topk - 1);
-            pos[u] = pos_of[i];
-            wgt[u] = wts[i];
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) // (a dropped slot: any row, not added)
-            d[u] = ldf4(D + (int64_t)max(pos[u], 0) * H + c);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (s0 + u >= topk || pos[u] < 0)
-                continue;
-            const float w = unit ? 1.f : wgt[u];
-            a0 = fmaf(w, d[u].x, a0);
-            a1 = fmaf(w, d[u].y, a1);
-            a2 = fmaf(w, d[u].z, a2);
-            a3 = fmaf(w, d[u].w, a3);
-        }
+    const int64_t first = (int64_t)t * topk;
+    float4_t a = {0.f, 0.f, 0.f, 0.f};
+    int s = 0;
+    for (; topk - s > (N == 8 ? 4 : 0); s += N)
+        combine_slots<N>(D, pos_of, wts, first, s, topk, H, c, unit, a);
+    if constexpr (N == 8) {
+        if (topk - s > 2)
+            combine_slots<4>(D, pos_of, wts, first, s, topk, H, c, unit, a);
+        else if (topk - s == 2)
+            combine_slots<2>(D, pos_of, wts, first, s, topk, H, c, unit, a);
+        else if (topk - s == 1)
+            combine_slots<1>(D, pos_of, wts, first, s, topk, H, c, unit, a);
     }
     *reinterpret_cast<uint2 *>(out + (int64_t)t * H + c) =
-        make_uint2(mx_pack2<BF16>(a0, a1), mx_pack2<BF16>(a2, a3));
+        make_uint2(mx_pack2<BF16>(a[0], a[1]), mx_pack2<BF16>(a[2], a[3]));
 }
 
 hipError_t launch_moe_group(const int32_t *ids, uint8_t *ws, const size_t *off, int64_t A,
@@ -262,18 +280,49 @@ hipError_t launch_moe_group(const int32_t *ids, uint8_t *ws, const size_t *off, 
     return hipGetLastError();
 }
 
+// Slots at a time: one where the device is full of workgroups (then the loads of others
+// hide a load's latency), else all up to four, rounded up to a power of two, or eight.
+// Measured, us for 1, 2, 4 and 8 at a time, hidden 2048: 4 tokens top-8 4.6, 3.9, 3.4, 3.0;
+// 256 tokens top-8 5.4, 4.7, 4.3, 4.4; 2048 tokens top-8 20.8, 21.2, 21.2, 21.2 (inside
+// the layer 21.4 and 22.6 for one and eight), top-2 7.6, 7.4, 7.5, 9.6, top-1 5.4, 5.8, 7.1, 9.4.
+static int combine_slots_at_once(int64_t blocks, int64_t topk)
+{
+    return topk == 1 || blocks > 8 * device_cus() ? 1 : topk == 2 ? 2 : topk <= 4 ? 4 : 8;
+}
+
+template <bool BF16>
+static void combine(const float *d, const int32_t *pos_of, const float *wts, uint16_t *out,
+                    int64_t T, int H, int topk, int unit, hipStream_t s)
+{
+    const int col_blocks = (H / 4 + 255) / 256;
+    const dim3 grid((unsigned)(T * col_blocks)), block(256);
+    switch (combine_slots_at_once(T * col_blocks, topk)) {
+    case 1:
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 1>), grid, block, 0, s, d, pos_of, wts, out, H,
+                           topk, col_blocks, unit);
+        break;
+    case 2:
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 2>), grid, block, 0, s, d, pos_of, wts, out, H,
+                           topk, col_blocks, unit);
+        break;
+    case 4:
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 4>), grid, block, 0, s, d, pos_of, wts, out, H,
+                           topk, col_blocks, unit);
+        break;
+    default:
+        hipLaunchKernelGGL((moe_combine_kernel<BF16, 8>), grid, block, 0, s, d, pos_of, wts, out, H,
+                           topk, col_blocks, unit);
+    }
+}
+
 hipError_t launch_moe_combine(const float *d, const int32_t *pos_of, const float *wts,
                               uint16_t *out, bool bf16, int64_t T, int64_t H, int64_t topk,
                               bool unit, hipStream_t s)
 {
-    const int col_blocks = (int)((H / 4 + 255) / 256);
-    const dim3 grid((unsigned)(T * col_blocks));
     if (bf16)
-        hipLaunchKernelGGL((moe_combine_kernel<true>), grid, dim3(256), 0, s, d, pos_of, wts, out,
-                           (int)H, (int)topk, col_blocks, (int)unit);
+        combine<true>(d, pos_of, wts, out, T, (int)H, (int)topk, (int)unit, s);
     else
-        hipLaunchKernelGGL((moe_combine_kernel<false>), grid, dim3(256), 0, s, d, pos_of, wts, out,
-                           (int)H, (int)topk, col_blocks, (int)unit);
+        combine<false>(d, pos_of, wts, out, T, (int)H, (int)topk, (int)unit, s);
     return hipGetLastError();
 }
 
