@@ -5,8 +5,7 @@ import numpy as np
 import pytest
 
 from quantized_unpack_q4_amd import gq
-from tests import _mxfp4 as mx
-from tests._gpu import dev, host, say, torch_cuda
+from tests._gpu import host
 from tests.test_gpu_mxfp4 import moe_case, moe_check
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +30,51 @@ def test_moe_combines_many_tokens(topk):
     """More workgroups than the device holds: one slot after another."""
     T, H, I, E = 2100, 64, 32, 8
     moe_check(moe_case(51, T, H, I, E, topk, "bf16"), T, H, I, E, topk, "bf16", False)
+
+
+def token_tile(ws, ids, E, H, I):
+    """Tokens of a tile of the expert products, from the tile list the layer left in its
+    workspace: checked against the counts for that tile."""
+    A = ids.size
+    up = lambda v: (v + 255) // 256 * 256
+    raw = host(ws)
+    o3 = up((E + 3) * 4) + 2 * up(A * 4)
+    ntiles = raw[:(E + 3) * 4].view(np.int32)[E + 1]
+    count = np.bincount(ids.reshape(-1), minlength=E)
+    fits = [bn for bn in (16, 64, 128, 256) if sum(-(-c // bn) for c in count) == ntiles]
+    # distinct counts of tiles tell the sizes apart
+    assert len(fits) == 1, (ntiles, count, fits)
+    first = raw[o3:o3 + 8 * (A + E)].view(np.int32)
+    assert sorted(first[:ntiles]) == sorted(np.repeat(np.arange(E), -(-count // fits[0])))
+    return fits[0]
+
+
+def counts_to_ids(seed, count, topk):
+    """Expert ids [T][topk] with so many slots of each expert, in a random order."""
+    ids = np.repeat(np.arange(len(count)), count)
+    return np.random.default_rng(seed).permutation(ids).reshape(-1, topk).astype(np.int32)
+
+
+# H and I choose how each product reads its scales: 16 bytes at a time (a multiple of 512), by
+# dwords (of 128) or byte by byte; 1536 is three chunks of 512 columns, both places in turn
+HI = [(1024, 1536), (512, 512), (1536, 640), (384, 2048), (160, 1056)]
+
+
+@pytest.mark.parametrize("t,iw", [("f16", False), ("bf16", True)])
+@pytest.mark.parametrize("H,I", HI)
+@pytest.mark.parametrize("tile,count,topk", [
+    (16, [20, 7, 1, 0, 16, 2], 2),   # the weight-streaming kernel
+    (64, [70, 1, 33, 24], 2),        # a full tile and a rest, one token, half a tile, less
+    (64, [64, 65, 3, 0, 28], 1),
+    (128, [150, 64, 65, 129], 2),    # rests of 22, 64, 65 and 1
+    (128, [128, 192, 40], 1),
+    (256, [296, 356], 1),            # rests of 40 and 100
+    (256, [320, 257, 576], 1),       # 64, 1 and 64 after two whole tiles
+    (256, [321, 512, 7], 2),         # 65, none, one short tile
+])
+def test_moe_tiles(tile, count, topk, H, I, iw, t):
+    E = len(count)
+    ids = counts_to_ids(1, count, topk)
+    T = len(ids)
+    _, ws = moe_check(moe_case(60, T, H, I, E, topk, t, ids), T, H, I, E, topk, t, iw)
+    assert token_tile(ws, ids, E, H, I) == tile
