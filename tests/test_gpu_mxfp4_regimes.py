@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 
 from quantized_unpack_q4_amd import gq
-from tests._gpu import host
-from tests.test_gpu_mxfp4 import moe_case, moe_check
+from tests import _mxfp4 as mx
+from tests._gpu import host, torch_cuda
+from tests.test_gpu_mxfp4 import as_type, check, moe_case, moe_check, normal, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,67 @@ def test_moe_tiles(tile, count, topk, H, I, iw, t):
     T = len(ids)
     _, ws = moe_check(moe_case(60, T, H, I, E, topk, t, ids), T, H, I, E, topk, t, iw)
     assert token_tile(ws, ids, E, H, I) == tile
+
+
+# -- products ------------------------------------------------------------------------
+
+def cus():
+    return torch_cuda().cuda.get_device_properties(0).multi_processor_count
+
+
+# one row tile of 16 a workgroup up to one per CU, two up to two per CU, then four; a wave
+# takes one step of 128 columns at a time below 16 steps, two below 32, then four
+FEW_ROWS = [(tiles, K) for tiles in (1, 2, 4) for K in (160, 2080, 4128)]
+
+
+def few_rows_m(tiles):
+    """A number of weight rows for so many tiles a workgroup, no tile or workgroup whole."""
+    return {1: 16 * cus() - 19, 2: 16 * cus() + 17, 4: 32 * cus() + 41}[tiles]
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 5, 16])
+@pytest.mark.parametrize("tiles,K", FEW_ROWS)
+def test_gemm_few_rows(tiles, K, N, t):
+    M = few_rows_m(tiles)
+    q, s, W = weights(61, M, K)
+    xd, x64 = as_type(normal(62, N, K), t)
+    y = gq.gemm_mxfp4(q, s, xd)
+    ref, S = mx.products(W, x64)
+    check(y, ref, S, t, "gemm %s %d %d %d" % (t, M, K, N))
+
+
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 5, 16])
+@pytest.mark.parametrize("tiles,K", FEW_ROWS)
+def test_mxgemm_few_rows(tiles, K, N, t):
+    torch = torch_cuda()
+    M = few_rows_m(tiles)
+    q, s, W = weights(63, M, K)
+    xq, xs, X = weights(64, N, K)
+    y = gq.gemm_mxfp4_mxfp4(q, s, xq, xs, dtype={"f32": torch.float32, "f16": torch.float16,
+                                                 "bf16": torch.bfloat16}[t])
+    ref, S = mx.products(W, X)
+    check(y, ref, S, t, "mxgemm %s %d %d %d" % (t, M, K, N))
+
+
+@pytest.mark.parametrize("K", [512, 1536, 544])
+def test_mxgemm_whole_and_half_tiles(K):
+    """18 x 16 tiles of 256 x 256 (on 256 CUs): 256 whole ones and 32 in halves, one launch."""
+    torch = torch_cuda()
+    M, N = 4500, 4000
+    q, s, W = weights(65, M, K)
+    xq, xs, X = weights(66, N, K)
+    y = gq.gemm_mxfp4_mxfp4(q, s, xq, xs, dtype=torch.bfloat16)
+    ref, S = mx.products(W, X)
+    check(y, ref, S, "bf16", "mxgemm whole and halves %d" % K)
+
+
+@pytest.mark.parametrize("K", [512, 1536, 640, 544])
+def test_gemm_whole_and_half_tiles(K):
+    M, N = 4500, 4000
+    q, s, W = weights(67, M, K)
+    xd, x64 = as_type(normal(68, N, K), "f16")
+    y = gq.gemm_mxfp4(q, s, xd)
+    ref, S = mx.products(W, x64)
+    check(y, ref, S, "f16", "gemm whole and halves %d" % K)
