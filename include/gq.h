@@ -521,6 +521,8 @@ gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, cons
                             uint16_t *out, int type, int64_t T, int64_t H, int64_t I, int64_t E,
                             int64_t topk, int64_t input_weighted, void *ws, size_t ws_bytes,
                             void *stream);
+/* Workspace size for gq_moe_gemm_mxfp4 with these sizes (0, and the reason in
+ * gq_last_error(), if the layer does not take them). */
 size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
 
 /* Diagnostics. */

@@ -57,6 +57,16 @@ gq_status product_checks(const char *fn, int64_t M, int64_t K, int64_t N)
     return check_most(fn, "M*N", M * N, kMaxOutputs);
 }
 
+// The sizes the expert layer takes, and its workspace's regions.
+gq_status moe_shape(const char *fn, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
+                    size_t off[7])
+{
+    GQ_TRY(moe_layout(fn, T, H, I, E, topk, 32, off));
+    GQ_TRY(check_most(fn, "H", H, kMaxK));
+    GQ_TRY(check_most(fn, "I", I, kMaxK));
+    return check_most(fn, "T*H", T * H, ((int64_t)1 << 31) - 1);
+}
+
 } // namespace
 
 extern "C" {
@@ -157,9 +167,10 @@ size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, 
     size_t off[7];
     char saved[sizeof g_err];
     memcpy(saved, g_err, sizeof g_err);
-    const gq_status st = moe_layout("gq_moe_mxfp4_workspace_bytes", T, H, I, E, topk, 32, off);
+    if (moe_shape("gq_moe_mxfp4_workspace_bytes", T, H, I, E, topk, off) != GQ_OK)
+        return 0;
     memcpy(g_err, saved, sizeof g_err);
-    return st == GQ_OK ? off[6] : 0;
+    return off[6];
 }
 
 gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, const uint8_t *wq_up,
@@ -172,10 +183,7 @@ gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, cons
     static const char fn[] = "gq_moe_gemm_mxfp4";
     gq::MxMoeArgs a{};
     GQ_TRY(check_type(fn, "type", type, false));
-    GQ_TRY(moe_layout(fn, T, H, I, E, topk, 32, a.off));
-    GQ_TRY(check_most(fn, "H", H, kMaxK));
-    GQ_TRY(check_most(fn, "I", I, kMaxK));
-    GQ_TRY(check_most(fn, "T*H", T * H, ((int64_t)1 << 31) - 1));
+    GQ_TRY(moe_shape(fn, T, H, I, E, topk, a.off));
     if (T == 0)
         return GQ_OK;
     GQ_TRY(check_ptr(fn, "wq_gate", wq_gate));
