@@ -511,8 +511,8 @@ gq_status gq_gemm_mxfp4_mxfp4(const uint8_t *wq, const uint8_t *ws, const uint8_
  * x, h and out of `type` (GQ_F16 or GQ_BF16) and weights as in gq_gemm_mxfp4.
  * wq_gate, wq_up: [E][I][H/2], ws_gate, ws_up: [E][I][H/32]; wq_down: [E][H][I/2],
  * ws_down: [E][H][I/32].  ws: at least gq_moe_mxfp4_workspace_bytes() bytes,
- * regions as in gq_moe_workspace_offsets; contents on entry are ignored; not to be
- * in use by another call while this one runs.  Requires H % 32 == 0,
+ * contents on entry are ignored; not to be in use by another call while this one
+ * runs.  Requires H % 32 == 0,
  * I % 32 == 0, H, I <= 2^22, 1 <= topk <= E <= 256, T*topk <= 2^20, T*H < 2^31.
  * Slots with an id outside [0, E) are skipped. */
 gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, const uint8_t *wq_up,
@@ -524,6 +524,10 @@ gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, cons
 /* Workspace size for gq_moe_gemm_mxfp4 with these sizes (0, and the reason in
  * gq_last_error(), if the layer does not take them). */
 size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+/* Byte offsets of its regions: those of gq_moe_workspace_offsets, h of `type`, for the
+ * sizes gq_moe_gemm_mxfp4 takes (that entry point takes multiples of 256 only). */
+gq_status gq_moe_mxfp4_workspace_offsets(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
+                                         size_t off[7]);
 
 /* Diagnostics. */
 const char *gq_last_error(void);       /* message of this thread's last failed call */

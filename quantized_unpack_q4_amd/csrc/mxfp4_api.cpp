@@ -173,6 +173,15 @@ size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, 
     return off[6];
 }
 
+gq_status gq_moe_mxfp4_workspace_offsets(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
+                                         size_t off[7])
+{
+    static const char fn[] = "gq_moe_mxfp4_workspace_offsets";
+    if (!off)
+        return fail(GQ_EINVAL, "%s: off is NULL", fn);
+    return moe_shape(fn, T, H, I, E, topk, off);
+}
+
 gq_status gq_moe_gemm_mxfp4(const uint8_t *wq_gate, const uint8_t *ws_gate, const uint8_t *wq_up,
                             const uint8_t *ws_up, const uint8_t *wq_down, const uint8_t *ws_down,
                             const uint16_t *x, const int32_t *topk_ids, const float *topk_w,

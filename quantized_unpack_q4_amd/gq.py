@@ -36,8 +36,8 @@ EXPORTS = (
     "gq_gemm_q4k_q8k",
     "gq_moe_workspace_bytes", "gq_moe_workspace_offsets", "gq_dequant_q8_0",
     "gq_dequant_q4k", "gq_quantize_mxfp4", "gq_dequant_mxfp4", "gq_gemv_mxfp4", "gq_gemm_mxfp4",
-    "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes", "gq_last_error",
-    "gq_status_str", "gq_version",
+    "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes",
+    "gq_moe_mxfp4_workspace_offsets", "gq_last_error", "gq_status_str", "gq_version",
 )
 
 
@@ -135,6 +135,8 @@ def lib() -> ctypes.CDLL:
         L.gq_moe_gemm_mxfp4.argtypes = [vp] * 10 + [ci] + [i64] * 6 + [vp, sz, vp]
         L.gq_moe_mxfp4_workspace_bytes.restype = sz
         L.gq_moe_mxfp4_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+        L.gq_moe_mxfp4_workspace_offsets.restype = st
+        L.gq_moe_mxfp4_workspace_offsets.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
         L.gq_last_error.restype = ctypes.c_char_p
         L.gq_last_error.argtypes = []
         L.gq_status_str.restype = ctypes.c_char_p
@@ -387,6 +389,12 @@ def gq_gemm_mxfp4_mxfp4(wq, ws, xq, xs, y, y_type, M, K, N, stream=None):
 
 def gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk) -> int:
     return int(lib().gq_moe_mxfp4_workspace_bytes(T, H, I, E, topk))
+
+
+def gq_moe_mxfp4_workspace_offsets(T, H, I, E, topk):
+    off = (ctypes.c_size_t * 7)()
+    _check(lib().gq_moe_mxfp4_workspace_offsets(T, H, I, E, topk, off))
+    return list(off)
 
 
 def gq_moe_gemm_mxfp4(wq_gate, ws_gate, wq_up, ws_up, wq_down, ws_down, x, topk_ids, topk_w, out,
