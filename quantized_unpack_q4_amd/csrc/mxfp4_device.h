@@ -65,6 +65,11 @@ __device__ __forceinline__ float4_t mx_mfma16_fp4(uint4 a, uint32_t sa, uint4 b,
                                                             (int)sb);
 }
 
+// Lanes of a wave hand values on through LDS without a barrier: the LDS keeps the order of a
+// wave's accesses, and this keeps it in the compiled code, which knows one lane's addresses
+// only.
+__device__ __forceinline__ void lds_wave_order() { asm volatile("" ::: "memory"); }
+
 // Two binary32 values rounded (nearest even) to the 16-bit type, packed.
 template <bool BF16>
 __device__ __forceinline__ uint32_t mx_pack2(float lo, float hi)

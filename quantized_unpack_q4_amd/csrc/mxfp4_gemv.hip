@@ -277,10 +277,12 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_wide_kernel(MxMat w, const
     };
     auto turn_x = [&]() {
         uint8_t *d = lds[wave] + 16 * lane;
+        lds_wave_order(); // after the reads of the unit before
 #pragma unroll
         for (int b = 0; b < 16; ++b)
             if (b < B)
                 *reinterpret_cast<float4 *>(d + b * kRow) = xr[b];
+        lds_wave_order();
     };
 
     float4_t acc[RT];
@@ -343,6 +345,7 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_gemv_wide_kernel(MxMat w, const
     }
 
     // lane l of a wave holds rows 4 (l / 16) + 0..3 of column l % 16
+    lds_wave_order();
 #pragma unroll
     for (int t = 0; t < RT; ++t)
         *reinterpret_cast<float4_t *>(lds[wave] + 1024 * t + 16 * lane) = acc[t];

@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
             *reinterpret_cast<uint2 *>(d) = make_uint2(mx_pack2<TYPE == kBF16>(v[g][0], v[g][1]),
                                                        mx_pack2<TYPE == kBF16>(v[g][2], v[g][3]));
     }
-    asm volatile("" ::: "memory"); // (the LDS keeps a wave's order)
+    lds_wave_order();
     const bool vec = M % CE == 0; // rows start 16-byte aligned
     const int64_t mleft = M - m;
 #pragma unroll
@@ -127,7 +127,7 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
                 }
         }
     }
-    asm volatile("" ::: "memory");
+    lds_wave_order();
 }
 
 } // namespace gq
