@@ -6,8 +6,8 @@ import pytest
 
 from quantized_unpack_q4_amd import gq
 from tests import _mxfp4 as mx
-from tests._gpu import host, torch_cuda
-from tests.test_gpu_mxfp4 import as_type, check, moe_case, moe_check, normal, weights
+from tests._gpu import dev, host, torch_cuda
+from tests.test_gpu_mxfp4 import as_type, check, moe_case, moe_check, normal, values64, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,51 @@ def test_gemm_whole_and_half_tiles(K):
     y = gq.gemm_mxfp4(q, s, xd)
     ref, S = mx.products(W, x64)
     check(y, ref, S, "f16", "gemm whole and halves %d" % K)
+
+
+# -- activations' range --------------------------------------------------------------
+
+@pytest.mark.parametrize("B", [1, 3, 5, 6, 16])
+@pytest.mark.parametrize("ex", [-149, -140, -133, -126, -120, -112, -60, 0, 60, 100])
+def test_gemv_whole_vectors_of_a_magnitude(ex, B):
+    """Activations from the smallest subnormal on, weights that bring the results to about
+    2^-20 or, for 1e-40 and the like, as near as scales go.  GQ_GEMV_ACCURACY: 1e-5 S, and a
+    few multiples of 2^-149 for results in the subnormal range: here one for every wave's
+    sum and every part (16 waves, 3 parts)."""
+    M, K = 48, 1056
+    lo = int(np.clip(127 - 20 - ex, 1, 240))
+    q, s = mx.weights(69, M, K, lo, lo + 8)
+    W = mx.values(q, s)
+    x = np.ldexp(normal(70, B, K), ex).astype(np.float32)
+    x[:, ::7] = 0.0
+    y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x)))
+    ref, S = mx.products(W, x.astype(np.float64))
+    bound = 1e-5 * S + 48 * 2.0 ** -149 + mx.EPS2["f32"] * np.abs(ref)
+    assert np.isfinite(y).all() and (np.abs(y - ref) <= bound).all(), (np.abs(y - ref) / bound).max()
+
+
+@pytest.mark.parametrize("B", [1, 3, 5, 6, 16])
+def test_gemv_results_in_the_subnormal_range(B):
+    """Products and sums below 2^-126: multiples of 2^-149, off by a rounding at each of the
+    additions that follow one another (K / 8 and the joins)."""
+    M, K = 48, 1056
+    q, s = mx.weights(71, M, K, 127 - 70, 127 - 66)
+    W = mx.values(q, s)
+    x = np.ldexp(normal(72, B, K), -66).astype(np.float32)
+    y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x)))
+    ref, S = mx.products(W, x.astype(np.float64))
+    assert (np.abs(y - ref) <= 1e-5 * S + (K // 8 + 48) * 2.0 ** -149).all()
+
+
+def test_gemv_near_the_largest_activations():
+    """The scaled parts stay finite: 2^127 and neighbours, weights far below one."""
+    M, K = 16, 64
+    q, s = mx.weights(73, M, K, 40, 44)
+    W = mx.values(q, s)
+    x = np.full((6, K), np.float32(3.4028235e38))
+    x[1] = np.nextafter(np.float32(2.0 ** 127), np.float32(0))
+    x[2] = -np.float32(1.2345678 * 2.0 ** 126)
+    for B in (1, 3, 6):
+        y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x[:B])))
+        ref, S = mx.products(W, x[:B].astype(np.float64))
+        assert (np.abs(y - ref) <= 1e-5 * S).all()
