@@ -456,12 +456,13 @@ gq_status gq_dequant_q4k(const void *w, float *out32, uint16_t *out16, int64_t M
 /* Microscaled 4-bit (MXFP4) operators: the same forms of the fused product over
  * MXFP4 weights (the planes described above; this library's own addition, the
  * pages name no such format).  An MXFP4 weight is exact in binary32 and in
- * bfloat16 for s <= 252 (above, values of 2^128 and more are infinities); in
- * binary16 it is exact for 104 <= s <= 140, else rounded once (nearest even,
- * overflow to infinity), as the other formats' weights are.  A
- * block with s = 255 makes every product it enters NaN; so do infinities in the
- * activations, except where the sums of the definition are infinite (either may
- * come back).
+ * bfloat16 for s <= 252 (above, values of 2^128 and more are infinities; the
+ * quantiser gives s <= 252 or 255); in binary16 it is exact for 104 <= s <= 140,
+ * else rounded once (nearest even, overflow to infinity), as the other formats'
+ * weights are: the operands of binary16 matrix products.  gq_gemm_mxfp4_mxfp4 takes
+ * every s up to 254 exactly.  A block with s = 255 makes every product it enters
+ * NaN.  An infinite weight makes the results it enters infinite or NaN, and so does
+ * an infinite activation.
  *
  * gq_quantize_mxfp4: per block of 32 values of a row,
  *   s = clamp(floor(log2(max|x|)) - 2, -127, 127) + 127,

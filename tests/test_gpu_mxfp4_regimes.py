@@ -191,3 +191,61 @@ def test_gemv_near_the_largest_activations():
         y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x[:B])))
         ref, S = mx.products(W, x[:B].astype(np.float64))
         assert (np.abs(y - ref) <= 1e-5 * S).all()
+
+
+# -- weights' range --------------------------------------------------------------------
+
+@pytest.mark.parametrize("N", [1, 6, 40])
+def test_weights_beyond_a_type_reach_their_rows_only(N):
+    """Row 3 has a block of infinite weights of the type (bfloat16, binary32: s = 253 with codes
+    of 4; binary16: s = 141 with codes of 4): its results are infinite or NaN, the others
+    and the product of two MXFP4 matrices are right."""
+    torch = torch_cuda()
+    M, K = 40, 160
+    q, s = mx.weights(74, M, K, 110, 120)
+    q[3, 16:32] = 0x66
+    rows = np.arange(M) != 3
+    x = np.abs(normal(75, N, K)) + 0.5
+    for t, sc in (("bf16", 253), ("f16", 141)):
+        s[3, 1] = sc
+        W = mx.values(q, s)
+        xd, x64 = as_type(x, t)
+        ys = [gq.gemm_mxfp4(dev(q), dev(s), xd)]
+        if t == "bf16" and N <= 16:
+            ys.append(gq.gemv_mxfp4(dev(q), dev(s), xd.float()))
+        ref, S = mx.products(W, x64)
+        for y in ys:
+            v = values64(y)
+            assert not np.isfinite(v[:, 3]).any()
+            f = "f32" if y.dtype == torch.float32 else t
+            bound = mx.EPS2[f] * np.abs(ref) + mx.TINY[f] + 1e-5 * S * (1 + mx.EPS2[f])
+            assert (np.abs(v - ref) <= bound)[:, rows].all()
+    # scales up to 254, against activations small enough for the results
+    s[3, 1] = 254
+    W = mx.values(q, s)
+    xq, xs = mx.weights(76, N, K, 20, 24)
+    ref, S = mx.products(W, mx.values(xq, xs))
+    v = values64(gq.gemm_mxfp4_mxfp4(dev(q), dev(s), dev(xq), dev(xs)))
+    assert (np.abs(v - ref) <= 1e-5 * S + mx.EPS2["f32"] * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("N", [1, 6, 40])
+@pytest.mark.parametrize("lo", [0, 1, 3])
+def test_smallest_weights(lo, N):
+    """Scales from 2^-127 on: subnormal numbers of bfloat16, exact like all others."""
+    M, K = 40, 160
+    q, s = mx.weights(77, M, K, lo, lo + 2)
+    W = mx.values(q, s)
+    xd, x64 = as_type(np.ldexp(normal(78, N, K), 100), "bf16")
+    ref, S = mx.products(W, x64)
+    check(gq.gemm_mxfp4(dev(q), dev(s), xd), ref, S, "bf16", "smallest weights")
+    if N <= 16:
+        check(gq.gemv_mxfp4(dev(q), dev(s), xd.float()), ref, S, "f32", "smallest weights")
+    xq, xs = mx.weights(79, N, K, 220, 224)
+    ref, S = mx.products(W, mx.values(xq, xs))
+    check(gq.gemm_mxfp4_mxfp4(dev(q), dev(s), dev(xq), dev(xs)), ref, S, "f32", "smallest weights")
+    # subnormal activations against large weights
+    q, s = mx.weights(80, M, K, 200, 204)
+    xd, x64 = as_type(np.ldexp(normal(81, N, K), -130), "bf16")
+    ref, S = mx.products(mx.values(q, s), x64)
+    check(gq.gemm_mxfp4(dev(q), dev(s), xd), ref, S, "bf16", "subnormal activations")
