@@ -3,6 +3,7 @@
 
 #include "gq_lds_dma.h"
 #include "mxfp4_device.h"
+#include "mxfp4_krun.h"
 
 namespace gq {
 
@@ -44,22 +45,6 @@ inline int tiles_whole(int64_t total, int64_t cus)
 inline unsigned tile_grid(int64_t total, int64_t whole)
 {
     return (unsigned)((whole + 7) / 8 * 8 + (2 * (total - whole) + 7) / 8 * 8);
-}
-
-// The run of K of one of KG groups of waves, in blocks of 32 columns: of the whole
-// chunks of `unit` blocks (the last may be short) group g takes every KG-th part, at
-// least one chunk each where there are KG.
-struct KRun {
-    int first, blocks, longest;
-};
-template <int KG>
-__device__ __forceinline__ KRun k_run(int nblk, int unit, int g)
-{
-    if (KG == 1)
-        return {0, nblk, nblk};
-    const int units = (nblk + unit - 1) / unit;
-    const int a = units * g / KG * unit, b = units * (g + 1) / KG * unit;
-    return {a, (b < nblk ? b : nblk) - a, (units + KG - 1) / KG * unit};
 }
 
 // Tile (tm, tn) number t: in groups of eight tile rows, columns one after another.

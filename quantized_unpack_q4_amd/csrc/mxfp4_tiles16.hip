@@ -29,10 +29,6 @@ namespace {
 
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
-// How a row's scales reach the lanes: 16 bytes (512 columns) at a time through LDS where
-// K % 512 == 0, by dwords through LDS where K % 128 == 0, else byte by byte.
-enum { kScale1 = 0, kScale4 = 1, kScale16 = 2 };
-
 struct Tile16Args {
     MxMat w, w2; // gate/up: gate, up
     const uint16_t *x;
@@ -93,7 +89,7 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
     const int r = lane & 31, h = lane >> 5;
     // this group's run of K: whole chunks of 256 (512) columns, at least one; the
     // groups step alike, as often as the longest
-    const KRun run = k_run<KG>(K >> 5, SM == kScale16 ? 16 : 8, kg);
+    const KRun run = k_run<KG>(K >> 5, SM, kg);
     const int nblk = run.blocks, nst = (nblk + 1) >> 1, nch = (nblk + 7) >> 3;
     const int steps = KG == 1 ? nst : (run.longest + 1) >> 1;
     lds += kg * lds_bytes(BM, BN, NB, SM);
@@ -481,14 +477,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void moe_tile16_kernel(Tile16
         tile16<BF16, MODE, WM, WN, KG, FM, FR, NB, SM>(p, m0, n0, nv, e, lds);
     else
         tile16<BF16, MODE, WM, WN, KG, FM, FN, NB, SM>(p, m0, n0, nv, e, lds);
-}
-
-// Whether KG groups of waves have a run of K each, and how its scales are read then.
-template <int KG>
-int scale_mode(int K)
-{
-    const int chunks = (K + 255) / 256;
-    return chunks < KG ? -1 : K % 512 == 0 && chunks >= 2 * KG ? kScale16 : K % 128 == 0 ? kScale4 : kScale1;
 }
 
 template <bool BF16, int MODE, int WM, int WN, int KG, int FM, int FN, int FR, int NB>
