@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64 * NW) void mxfp4_skinny_kernel(SkinnyArgs p)
             for (int w = 1; w < NW; ++w)
                 a[t] += red[w][NMAT * i + t][ln];
         }
-        if constexpr (MODE == kGateUp) {
+        if constexpr (MODE == kGateUp) { // (h goes to 16 bits: see mxfp4_tiles16.hip)
             const float pw = p.weight_input ? p.wts[p.sorted[n0 + n]] : 1.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)

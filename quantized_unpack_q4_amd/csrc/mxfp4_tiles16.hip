@@ -14,7 +14,16 @@
 // Conversions and LDS reads are one product ahead of the matrix instructions.
 //
 // Gate/up: fragment 0 of a wave holds rows of the gate matrix, fragment 1 the same
-// rows of the up matrix, so h = silu(g) u is formed in registers.
+// rows of the up matrix, so h = silu(g) u is formed in registers.  It is stored in the
+// activations' 16-bit type, the operand of the down product (the layer's formula; the Q4_K
+// and Q8_0 layers round it alike): a second 16-bit part would double that product's matrix
+// instructions, a third more for the layer, and the traffic of h.  The error of the layer is
+// 1.4 times that with h in binary32 (64 experts, top-8, hidden 2048, intermediate 1024, mean
+// over the outputs: bfloat16 2.3e-3 and 1.7e-3, binary16 2.9e-4 and 2.1e-4).
+//
+// Binary16 weights are rounded where binary16 does not hold them (scales below 104 and above
+// 140; layers have 110 to 130): the matrix instructions take both operands in one type, and
+// bfloat16 parts of binary16 activations would be two products for one.
 #include <algorithm>
 #include <type_traits>
 

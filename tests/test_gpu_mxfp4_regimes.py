@@ -249,3 +249,29 @@ def test_smallest_weights(lo, N):
     xd, x64 = as_type(np.ldexp(normal(81, N, K), -130), "bf16")
     ref, S = mx.products(mx.values(q, s), x64)
     check(gq.gemm_mxfp4(dev(q), dev(s), xd), ref, S, "bf16", "subnormal activations")
+
+
+@pytest.mark.parametrize("tokens", [4, 60, 300])
+def test_moe_h_beyond_binary16(tokens):
+    """h of one token above 65504: infinite in binary16, and with it that token's outputs;
+    the others as ever, and all of them finite in bfloat16."""
+    H, I, E, topk = 128, 96, 2, 1
+    for t in ("bf16", "f16"):
+        st = moe_case(82, tokens, H, I, E, topk, t)
+        x = st["x"].clone()
+        x[1] *= 8192.0
+        st["x"], st["X"] = x, values64(x)
+        flat = st["ids"].reshape(-1)
+        W = [st["W" + n][flat[1]] for n in "gu"]
+        g, u = (st["X"][1] @ w.T for w in W)
+        assert np.abs(g / (1 + np.exp(-np.clip(g, -700, 700))) * u).max() > 2 * 65504
+        if t == "bf16":
+            out, _ = moe_check(st, tokens, H, I, E, topk, t, False)
+            assert np.isfinite(values64(out)).all()
+        else:
+            out, _ = gq.moe_mxfp4(st["g"], st["u"], st["d"], st["x"], dev(st["ids"]), dev(st["wts"]))
+            v = values64(out)
+            assert not np.isfinite(v[1]).any() and np.isfinite(np.delete(v, 1, 0)).all()
+            x[1] = 0.0  # the other tokens' outputs do not depend on it
+            alone, _ = gq.moe_mxfp4(st["g"], st["u"], st["d"], x, dev(st["ids"]), dev(st["wts"]))
+            assert np.array_equal(np.delete(values64(alone), 1, 0), np.delete(v, 1, 0))
