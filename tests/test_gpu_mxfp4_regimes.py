@@ -275,3 +275,29 @@ def test_moe_h_beyond_binary16(tokens):
             x[1] = 0.0  # the other tokens' outputs do not depend on it
             alone, _ = gq.moe_mxfp4(st["g"], st["u"], st["d"], x, dev(st["ids"]), dev(st["wts"]))
             assert np.array_equal(np.delete(values64(alone), 1, 0), np.delete(v, 1, 0))
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("count", [[3, 9, 4, 2], [70, 1, 33, 24], [150, 64, 65, 129], [321, 512, 7, 300]])
+def test_moe_nan_and_infinity_stay_with_their_token_and_expert(count, t):
+    """The streaming kernel and each token tile: a NaN or infinity in a token, a block of NaN
+    weights in an expert."""
+    H, I, E = 160, 96, len(count)
+    ids = counts_to_ids(2, count, 1)
+    T = len(ids)
+    st = moe_case(83, T, H, I, E, 1, t, ids)
+    clean, _ = moe_check(st, T, H, I, E, 1, t, False)
+    clean = values64(clean)
+    x = st["x"].clone()
+    x[T // 2, H - 1] = float("nan")
+    x[T - 1, 0] = float("inf")
+    out, _ = gq.moe_mxfp4(st["g"], st["u"], st["d"], x, dev(st["ids"]), dev(st["wts"]))
+    v = values64(out)
+    hit = np.isin(np.arange(T), [T // 2, T - 1])
+    assert not np.isfinite(v[hit]).any() and np.array_equal(v[~hit], clean[~hit])
+    st["d"][1][1, 5, I // 32 - 1] = 255  # the last block of row 5 of expert 1's down matrix
+    out, _ = gq.moe_mxfp4(st["g"], st["u"], st["d"], st["x"], dev(st["ids"]), dev(st["wts"]))
+    v = values64(out)
+    hit = np.zeros(v.shape, bool)
+    hit[ids[:, 0] == 1, 5] = True
+    assert np.isnan(v[hit]).all() and np.array_equal(v[~hit], clean[~hit])
