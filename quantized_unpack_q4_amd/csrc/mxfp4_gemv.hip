@@ -12,8 +12,8 @@
 // NaN in the second part (infinity minus infinity), so its row's results are NaN.  The
 // factors keep the parts of activations below 2^-109 above the last place of bfloat16,
 // 2^-133 (unscaled, 1e-36 is off by 2e-5 of itself and 1e-40 by 4 %); they cost a sum for
-// each part and 7 % of the time at batch 6 to 16 (4096 x 14336 batch 16 27.4 -> 29.5 us from
-// HBM), nothing up to five rows, whose parts are columns with sums of their own.
+// each part and 7 % of the time at batch 6 to 16 (4096 x 14336 batch 16 27.4 -> 29.5 us,
+// weights from HBM), nothing up to five rows, whose parts are columns with sums of their own.
 //
 // In a step of 128 columns lane (c, h) takes block h of weight row c, converted with its
 // scale, and feeds four 16x16x32 products whose k order is permuted alike for both operands
@@ -400,12 +400,13 @@ hipError_t launch_gemv_mxfp4(MxMat w, const float *x, float *y, int64_t M, int64
                              hipStream_t st)
 {
     // Tiles of 16 rows shared out among the CUs (the activations are split once for a
-    // workgroup's or wave's).  Measured, us.  Up to five rows, one tile of 8 waves, of 16
-    // waves, two tiles of 8 waves: 4096 x 4096 batch 1 5.6, 6.3, 7.5, batch 4 7.0, 6.3, 8.5;
-    // 4096 x 14336 batch 1 12.5, 11.5, 18; 14336 x 4096 batch 1 12.1, 20, 12.0, batch 4 16, 20,
-    // 13.7; units of four, two and one steps 4096 x 4096 batch 1 5.6, 6.3, 7.5.  More rows, one,
-    // two and four tiles: 4096 x 14336 batch 16 27, 32, 46 (parts staged for all waves: 30);
-    // 6144 x 4096 18, 12.6, 16.5 (13.6); 14336 x 4096 34, 23, 18 (23).
+    // workgroup's or wave's).  Measured, us, weights from HBM.  Up to five rows, units of two
+    // steps, one tile of 8 waves, of 16 waves, two tiles of 8 waves: 4096 x 4096 batch 1 6.5,
+    // 6.5, 7.7, batch 4 7.3, 6.7, 8.7; 4096 x 14336 batch 1 13.6, 11.4, 17.6, batch 4 18, 15.5,
+    // 23; 14336 x 4096 batch 1 13.7, 20.9, 12.1, batch 4 16.7, 21, 14.0.  Units of four, two
+    // and one steps, one tile of 8 waves, batch 1: 4096 x 4096 5.9, 6.5, 7.6; 4096 x 2048 4.8, 4.7,
+    // 5.9.  More rows, one, two and four tiles, batch 16: 4096 x 14336 30, 34, 48; 6144 x 4096
+    // 20.7, 14.2, 17.9; 14336 x 4096 39, 26, 19.4.
     const int64_t tiles = (M + 15) / 16, cus = device_cus();
     if (B > 5)
         return tiles > 2 * cus ? launch_wide<4>(w, x, y, M, K, B, st)

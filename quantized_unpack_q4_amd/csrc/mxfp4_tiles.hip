@@ -9,8 +9,8 @@
 // row and stage for four or eight bytes of scales would cost as much as the codes.
 //
 // What bounds it, on 256 x 256 tiles at 4096 x 14336 by 4096 rows: the matrix cores
-// under the power limit.  The kernel takes 109 us (4.4 PFLOP/s); the same products on
-// unchanging registers, without copies and LDS reads, take 94 us.  Steps that got there
+// under the power limit.  The kernel takes 112 us (4.3 PFLOP/s; 119 with the weights from
+// HBM); the same products on unchanging registers, without copies and LDS reads, take 94 us.  Steps that got there
 // (same shape): stages of 128 columns with the scales by dwords 152 us (bound by requests
 // to the L2), 128-byte rows and 16-byte scales 130, operands read a step ahead with the
 // products pinned between the reads 117, copies spread between the products 113, results
@@ -37,8 +37,8 @@ namespace {
 
 struct TileArgs {
     MxMat w;
-    const void *x;     // activations: codes, or 16-bit
-    const uint8_t *xs; // scales of MXFP4 activations
+    const void *x;     // activations: codes
+    const uint8_t *xs; // and scales
     void *y;
     int ytype;
     int M, K, N;
@@ -295,7 +295,7 @@ __device__ __forceinline__ void mx_tile(const TileArgs &p, int m0, int n0, uint8
 }
 
 // Whether a launch of these tiles may cut its last ones: the 256-row ones (14336 x 4096 by
-// 4096 rows, 3.5 rounds, 133 -> 126 us; smaller tiles won nothing).
+// 4096 rows, 3.5 rounds, 133 -> 130 us; smaller tiles won nothing).
 constexpr bool cuts(int FM) { return FM == 4; }
 
 template <int WM, int WN, int FM, int FN, int NB, bool SL>
@@ -345,8 +345,8 @@ hipError_t launch_mx(TileArgs p, hipStream_t st)
 // (56 stages): 64 x 64 tiles 22 up to one per CU (one stage in flight 44), 41 at two, 71 at
 // four; 128 x 128 35 alone, 45 at one per CU (one stage in flight 53, 58), 79 at two;
 // 256 x 256 59-70 for a round in halves, 85 alone, 110-120 a full round.  So 4096 x 14336
-// takes by 130 rows 22 us on the first (36, 59 on the others), by 1024 rows 45 on the second
-// (71, 66), by 2048 rows 70 on the third (127, 79).
+// takes by 130 rows 24 us on the first (42, 60 on the others), by 1024 rows 46 on the second
+// (78, 67), by 2048 rows 73 on the third (148, 88).
 static int mx_tile_choice(int64_t M, int64_t N)
 {
     const int64_t cus = device_cus();

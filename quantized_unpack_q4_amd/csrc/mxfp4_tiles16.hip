@@ -436,7 +436,7 @@ __device__ __forceinline__ void tile16(const Tile16Args &p, int m0, int n0, int 
 }
 
 // Whether a launch of these tiles may cut its last ones: the 256-row ones.  14336 x 4096 by
-// 4096 rows (3.5 rounds) 375 -> 356 us; 128-row tiles lost 2-4 % to the second body at
+// 4096 rows (3.5 rounds) 375 -> 367 us; 128-row tiles lost 2-4 % to the second body at
 // most shapes.
 constexpr bool cuts(int FN) { return FN == 4; }
 
@@ -548,9 +548,9 @@ hipError_t launch_moe_pair(const MxMoeArgs &a, int max_tiles, hipStream_t st)
 // alone and full: 256 x 256 214, 350; 256 x 128 169, 188; 128 x 128 106, 115 (one stage in
 // flight 165, and 197 for two a CU); 128 x 64 with K in two runs 61, 68 (72); 64 x 64 in two
 // runs 40, 44 (one stage, four runs 53, 57); 64 x 32 in four runs 30, 28.  So 4096 x 14336
-// takes by 64 rows 31 us on 64 x 32 tiles (43, 62 on the next), by 130 rows 40 on 64 x 64
-// (53, 61), by 512 rows 68 on 128 x 64 (85, 106), by 1024 rows 115 on 128 x 128 (129, 169),
-// by 2048 rows 188 on 256 x 128 (219, 228); 14336 x 4096 by 1024 rows 95 on 256 x 256 (109).
+// takes by 64 rows 32 us on 64 x 32 tiles (45, 65 on the next), by 130 rows 45 on 64 x 64
+// (55, 64), by 512 rows 69 on 128 x 64 (88, 112), by 1024 rows 117 on 128 x 128 (130, 171),
+// by 2048 rows 190 on 256 x 128 (196, 227); 14336 x 4096 by 1024 rows 92 on 256 x 256 (112).
 int tile16_choice(int64_t M, int64_t K, int64_t N)
 {
     const int64_t cus = device_cus(), chunks = (K + 255) / 256;
