@@ -483,7 +483,7 @@ gq_status gq_dequant_mxfp4(const uint8_t *q, const uint8_t *s, void *out, int ou
 
 /* MXFP4 matrix-vector product, binary32 activations, 1 <= B <= GQ_GEMV_MAX_BATCH:
  *   y[b][r] = sum_k w[r][k] * x[b][k], products exact, sums binary32
- * (GQ_GEMV_ACCURACY, subnormal x included).
+ * (GQ_GEMV_ACCURACY for x as given, of subnormal x for the multiple of 2^-148 below).
  * wq: [M][K/2], ws: [M][K/32], x: [B][K], y: [B][M].  Requires K % 32 == 0,
  * K <= 2^22, M <= 2^26. */
 gq_status gq_gemv_mxfp4(const uint8_t *wq, const uint8_t *ws, const float *x, float *y, int64_t M,

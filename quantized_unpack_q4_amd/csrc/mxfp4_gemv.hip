@@ -5,15 +5,17 @@
 // whole blocks (16 bytes of codes, one scale) several steps ahead, the first before
 // anything else.
 //
-// Binary32 activations are split into three bfloat16 parts, x = a + 2^-8 b + 2^-16 c exactly
-// (8 + 8 + 8 significant bits, each part cut toward zero from what is left), and an
-// MXFP4 weight is a bfloat16 number exactly (s <= 252), so the products are exact and
-// only the binary32 sums of the matrix cores round.  An infinite or NaN activation leaves a
-// NaN in the second part (infinity minus infinity), so its row's results are NaN.  The
-// factors keep the parts of activations below 2^-109 above the last place of bfloat16,
-// 2^-133 (unscaled, 1e-36 is off by 2e-5 of itself and 1e-40 by 4 %); they cost a sum for
-// each part and 7 % of the time at batch 6 to 16 (4096 x 14336 batch 16 27.4 -> 29.5 us,
-// weights from HBM), nothing up to five rows, whose parts are columns with sums of their own.
+// Binary32 activations are split into three bfloat16 parts, x = a + 2^-7 b + 2^-15 c exactly
+// (8 + 8 + 8 significant bits, each part cut toward zero from what is left; of subnormal
+// activations the last bit, 2^-149, may be lost), and an MXFP4 weight is a bfloat16 number
+// exactly (s <= 252), so the products are exact and only the binary32 sums of the matrix
+// cores round.  An infinite or NaN activation leaves a NaN in the second part (infinity
+// minus infinity), so its row's results are NaN.  The factors keep the parts of activations
+// below 2^-109 above the last place of bfloat16, 2^-133 (unscaled, 1e-36 is off by 2e-5 of
+// itself and 1e-40 by 4 %), and no part above x itself, so that the parts' sums overflow
+// only where the whole may; they cost a sum for each part and 6 to 12 % of the time at batch 6
+// to 16 (4096 x 14336 batch 16 26.4 -> 28.6 us, weights from HBM), nothing up to five rows,
+// whose parts are columns with sums of their own.
 //
 // In a step of 128 columns lane (c, h) takes block h of weight row c, converted with its
 // scale, and feeds four 16x16x32 products whose k order is permuted alike for both operands
@@ -39,7 +41,7 @@ __host__ __device__ constexpr int chunk_columns(int NW, int B) { return 1024 * N
 constexpr int x_bytes(int NW) { return 6 * 1024 * NW + 15 * 16; }
 
 // What the second and third part are worth.
-constexpr float kPart2 = 0x1p-8f, kPart3 = 0x1p-16f;
+constexpr float kPart2 = 0x1p-7f, kPart3 = 0x1p-15f;
 
 // The three bfloat16 parts of four binary32 values, packed.
 __device__ __forceinline__ void split3(const float4 v, uint2 &a, uint2 &b, uint2 &c)
@@ -47,9 +49,9 @@ __device__ __forceinline__ void split3(const float4 v, uint2 &a, uint2 &b, uint2
     const float x[4] = {v.x, v.y, v.z, v.w};
     uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) { // each part is below the last place of the one before: no overflow
+    for (int j = 0; j < 4; ++j) { // (a rest is below the last place of the part before it)
         hi[j] = __builtin_bit_cast(uint32_t, x[j]);
-        const float r = (x[j] - __builtin_bit_cast(float, hi[j] & 0xffff0000u)) * 0x1p8f;
+        const float r = (x[j] - __builtin_bit_cast(float, hi[j] & 0xffff0000u)) * 0x1p7f;
         mid[j] = __builtin_bit_cast(uint32_t, r);
         lo[j] = __builtin_bit_cast(uint32_t, (r - __builtin_bit_cast(float, mid[j] & 0xffff0000u)) * 0x1p8f);
     }

@@ -153,7 +153,8 @@ def test_gemv_whole_vectors_of_a_magnitude(ex, B):
     """Activations from the smallest subnormal on, weights that bring the results to about
     2^-20 or, for 1e-40 and the like, as near as scales go.  GQ_GEMV_ACCURACY: 1e-5 S, and a
     few multiples of 2^-149 for results in the subnormal range: here one for every wave's
-    sum and every part (16 waves, 3 parts)."""
+    sum and every part (16 waves, 3 parts).  Of an activation 2^-149 may be lost: its third part
+    ends at 2^-148."""
     M, K = 48, 1056
     lo = int(np.clip(127 - 20 - ex, 1, 240))
     q, s = mx.weights(69, M, K, lo, lo + 8)
@@ -162,7 +163,7 @@ def test_gemv_whole_vectors_of_a_magnitude(ex, B):
     x[:, ::7] = 0.0
     y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x)))
     ref, S = mx.products(W, x.astype(np.float64))
-    bound = 1e-5 * S + 48 * 2.0 ** -149 + mx.EPS2["f32"] * np.abs(ref)
+    bound = 1e-5 * S + 48 * 2.0 ** -149 + mx.EPS2["f32"] * np.abs(ref) + 2.0 ** -149 * np.abs(W).sum(1)
     assert np.isfinite(y).all() and (np.abs(y - ref) <= bound).all(), (np.abs(y - ref) / bound).max()
 
 
@@ -191,6 +192,25 @@ def test_gemv_near_the_largest_activations():
         y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x[:B])))
         ref, S = mx.products(W, x[:B].astype(np.float64))
         assert (np.abs(y - ref) <= 1e-5 * S).all()
+
+
+@pytest.mark.parametrize("B", [1, 3, 5, 6, 16])
+@pytest.mark.parametrize("value", [2.0 ** 126 * (1 + 2.0 ** -7 - 2.0 ** -22), 2.0 ** 126 * (1 + 2.0 ** -8 - 2.0 ** -22),
+                                   2.0 ** 126 * (2 - 2.0 ** -22), 2.0 ** 126 * (1 + 2.0 ** -15 - 2.0 ** -22)])
+def test_gemv_results_in_the_highest_binade(value, B):
+    """Sums just below the largest number: the parts' sums stay below them.  Three weights of
+    one (a single one where three would pass it)."""
+    M, K = 16, 64
+    n = 3 if 3 * value < 3.4e38 else 1
+    q = np.zeros((M, K // 2), np.uint8)
+    q[:, :n] = 0x02
+    s = np.full((M, K // 32), 127, np.uint8)
+    x = np.zeros((B, K), np.float32)
+    x[:, :2 * n:2] = np.float32(value)
+    x[:, 1::2] = np.float32(-value)  # against zero weights
+    y = values64(gq.gemv_mxfp4(dev(q), dev(s), dev(x)))
+    ref = n * np.float64(np.float32(value))
+    assert (np.abs(y - ref) <= 1e-5 * ref).all()
 
 
 # -- weights' range --------------------------------------------------------------------
