@@ -9,7 +9,7 @@
 // row and stage for four or eight bytes of scales would cost as much as the codes.
 //
 // What bounds it, on 256 x 256 tiles at 4096 x 14336 by 4096 rows: the matrix cores
-// under the power limit.  The kernel takes 112 us (4.3 PFLOP/s; 119 with the weights from
+// under the power limit.  The kernel takes 111 us (4.3 PFLOP/s; 117 with the weights from
 // HBM); the same products on unchanging registers, without copies and LDS reads, take 94 us.  Steps that got there
 // (same shape): stages of 128 columns with the scales by dwords 152 us (bound by requests
 // to the L2), 128-byte rows and 16-byte scales 130, operands read a step ahead with the
