@@ -10,11 +10,11 @@
 //
 // What bounds it, on 256 x 256 tiles at 4096 x 14336 by 4096 rows: the matrix cores
 // under the power limit.  The kernel takes 111 us (4.3 PFLOP/s; 117 with the weights from
-// HBM); the same products on unchanging registers, without copies and LDS reads, take 94 us.  Steps that got there
-// (same shape): stages of 128 columns with the scales by dwords 152 us (bound by requests
-// to the L2), 128-byte rows and 16-byte scales 130, operands read a step ahead with the
-// products pinned between the reads 117, copies spread between the products 113, results
-// stored through LDS 109.
+// HBM); the same products on unchanging registers, without copies and LDS reads, take
+// 94 us.  Steps that got there (same shape): stages of 128 columns with the scales by
+// dwords 152 us (bound by requests to the L2), 128-byte rows and 16-byte scales 130,
+// operands read a step ahead with the products pinned between the reads 117, copies spread
+// between the products 113, results stored through LDS 109 (111 in the last trace).
 //
 // LDS rows are 128 bytes (eight blocks); block c of row r sits in slot
 // c ^ ((r >> 1) & 7): the 16 lanes of a read phase touch 16 rows and 16 distinct

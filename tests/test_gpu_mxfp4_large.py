@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.fixture(autouse=True)
-def free_memory():
+def seeded_and_freed():
+    torch_cuda().manual_seed(89)
     yield
     torch_cuda().cuda.empty_cache()
 
