@@ -534,6 +534,116 @@ size_t gq_moe_mxfp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, 
 gq_status gq_moe_mxfp4_workspace_offsets(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
                                          size_t off[7]);
 
+/* 8-bit integer (int8) matrices with a binary32 scale for each row: activations with a scale
+ * per token, weights with one per output channel (this library's own addition; the pages name
+ * no such format).  A matrix is codes int8 [rows][ld], of which K of every row count, and
+ * scales [rows]; a value is s[row] * q[row][k].  Rows of codes are ld bytes apart, ld a
+ * multiple of 16 and at least K; every row, the last included, has the bytes up to the next
+ * multiple of 16 behind its K codes in its allocation (they may hold anything and are never
+ * written).  All codes from -128 to 127 are taken.
+ *
+ * The products sum whole numbers: K <= 131071, so that sums fit 32 bits; every result is
+ *   (binary32(sum) * ws) * xs, three binary32 roundings, then one to the output's type,
+ * whatever kernel ran.  A NaN or infinite scale makes the results it enters NaN or infinite.
+ *
+ * gq_quantize_i8: per row of x,
+ *   s = max|x| / 127 (binary32),  q = 127 x / max|x| rounded to the nearest whole number
+ *   (halves to even), decided exactly.
+ * A zero row has s = 0; a row holding an infinity or a NaN has s = NaN and zero codes.  Scales
+ * below 2^-126 (rows below 1.5e-36) are subnormal and carry fewer bits.  x: N rows of K
+ * elements of x_type (any gq_dtype), ldx elements apart, ldx >= K (unused when N is 1; rows
+ * need no alignment).  q: [N][ldq], s: [N].  Requires N*K <= 2^34, ldx, ldq <= 2^40; q and s
+ * must not overlap x. */
+gq_status gq_quantize_i8(const void *x, int x_type, int64_t ldx, int8_t *q, int64_t ldq, float *s,
+                         int64_t N, int64_t K, void *stream);
+
+/* The values of an int8 matrix: out [M][K] of out_type (any gq_dtype), the binary32 product
+ * s * q rounded to that type.  Requires M*K <= 2^34, ldq <= 2^40. */
+gq_status gq_dequant_i8(const int8_t *q, int64_t ldq, const float *s, void *out, int out_type,
+                        int64_t M, int64_t K, void *stream);
+
+/* int8 matrix-vector product for 1 <= B <= GQ_GEMV_MAX_BATCH activation rows, each quantised
+ * on the way as by gq_quantize_i8 (the same results as that and gq_gemm_i8, bit for bit, in
+ * one launch):
+ *   y[b][r] = sum_k w[r][k] * v(x)[b][k].
+ * x: [B][K] and y: [B][M], both of `type` (any gq_dtype).  Requires K <= 131071, M <= 2^26,
+ * ldw <= 2^22. */
+gq_status gq_gemv_i8(const int8_t *wq, int64_t ldw, const float *ws, const void *x, void *y,
+                     int type, int64_t M, int64_t K, int64_t B, void *stream);
+
+/* The product of two int8 matrices on the int8 matrix cores, any number of activation rows:
+ *   Y[n][r] = xs[n] ws[r] sum_k xq[n][k] wq[r][k].
+ * y: [N][M] of y_type (any gq_dtype).  Requires K <= 131071, M <= 2^26, N <= 2^21,
+ * M*N <= 2^37, ldw, ldx <= 2^22. */
+gq_status gq_gemm_i8(const int8_t *wq, int64_t ldw, const float *ws, const int8_t *xq, int64_t ldx,
+                     const float *xs, void *y, int y_type, int64_t M, int64_t K, int64_t N,
+                     void *stream);
+
+/* The gradient of that product for the activations' values (weights are frozen; the rounding
+ * to codes passes gradients unchanged), for training what feeds quantised layers:
+ *   dX[n][k] = round( sum_m dY[n][m] * w16[m][k] ), sums binary32, one rounding,
+ * w16 = ws[m] * wq[m][k] rounded to `type` (GQ_F16 or GQ_BF16; the weights of the other
+ * 16-bit products are rounded so, too).  dy: [N] rows of M elements of `type`, ldd >= M
+ * elements apart (ldd unused when N is 1; rows need no alignment).  dx: [N][K] of `type`.
+ * Requires K <= 131071, 1 <= M <= 2^22, ldd <= 2^22, N <= 2^21, N*K <= 2^37, ldw <= 2^22. */
+gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, const uint16_t *dy,
+                              int64_t ldd, uint16_t *dx, int type, int64_t M, int64_t K, int64_t N,
+                              void *stream);
+
+/* Activations of the gated feed-forward block: act(z) = z sigmoid(p(z)). */
+typedef enum gq_act {
+    GQ_SILU = 0, /* p = z */
+    GQ_GELU = 1  /* p = 2 sqrt(2/pi) (z + 0.044715 z^3): GELU in its tanh form */
+} gq_act;
+
+/* The gate and up products of a feed-forward layer, the activation and the elementwise
+ * product in one launch, from int8 activations:
+ *   h[n][i] = round( act(g) * u ),  g = W_gate x, u = W_up x as gq_gemm_i8 forms them in
+ *   binary32, the epilogue in binary32.
+ * wq_gate, wq_up: I rows of H codes.  xq, xs: N rows of H codes.  h: [N][I] of h_type (any
+ * gq_dtype).  Requires the limits of gq_gemm_i8 for M = I, K = H; I = 0 or N = 0 launches
+ * nothing. */
+gq_status gq_gated_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,
+                      const int8_t *wq_up, int64_t ld_up, const float *ws_up, const int8_t *xq,
+                      int64_t ldx, const float *xs, void *h, int h_type, int act, int64_t I,
+                      int64_t H, int64_t N, void *stream);
+
+/* Its backward pass, for the activations' values (as gq_gemm_i8_backward):
+ *   dg = dh * u * act'(g),  du = dh * act(g), formed in binary32 from g and u, which are
+ *   computed again, and rounded to `type`;
+ *   dX[n][k] = round( sum_i dg[n][i] * w16_gate[i][k] + du[n][i] * w16_up[i][k] ).
+ * dh: [N][I] and dx: [N][H], both of `type` (GQ_F16 or GQ_BF16).  dg and du are rounded to the
+ * 16-bit type because they are operands of 16-bit matrix products, as a gradient held between
+ * two layers is.  ws: at least gq_gated_i8_backward_workspace_bytes() bytes, 16-byte aligned,
+ * contents on entry ignored; not to be in use by another call while this one runs.  Requires
+ * the limits of gq_gated_i8, 1 <= I <= 2^21 and N*H <= 2^37. */
+gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,
+                               const int8_t *wq_up, int64_t ld_up, const float *ws_up,
+                               const int8_t *xq, int64_t ldx, const float *xs, const uint16_t *dh,
+                               uint16_t *dx, int type, int act, int64_t I, int64_t H, int64_t N,
+                               void *ws, size_t ws_bytes, void *stream);
+/* Its workspace size (0, and the reason in gq_last_error(), for sizes it does not take; 0 where
+ * there is no work). */
+size_t gq_gated_i8_backward_workspace_bytes(int64_t N, int64_t H, int64_t I);
+
+/* The whole gated feed-forward block over int8 weights, forward:
+ *   h = round( act(W_gate v(x)) * W_up v(x) ), held in `type`;  out = W_down v(h),
+ * v() the values gq_quantize_i8 leaves of each row.  h is rounded to the 16-bit type before
+ * its codes are taken, as the expert layers hold it (with bfloat16 that rounding is about as
+ * large as a third of a code's step at the largest values and smaller below).
+ * wq_gate, wq_up: I rows of H codes; wq_down: H rows of I codes.  x, out: [T][H] of `type`
+ * (GQ_F16 or GQ_BF16).  A binary16 h above 65504 is infinite and its token's outputs NaN.  ws:
+ * at least gq_ffn_i8_workspace_bytes() bytes, 16-byte aligned, contents on entry ignored; not
+ * to be in use by another call while this one runs.  Requires 1 <= H, I <= 131071, T <= 2^21,
+ * T*H, T*I <= 2^34, ld_* <= 2^22. */
+gq_status gq_ffn_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,
+                    const int8_t *wq_up, int64_t ld_up, const float *ws_up, const int8_t *wq_down,
+                    int64_t ld_down, const float *ws_down, const uint16_t *x, uint16_t *out,
+                    int type, int act, int64_t T, int64_t H, int64_t I, void *ws, size_t ws_bytes,
+                    void *stream);
+/* Its workspace size (0, and the reason in gq_last_error(), for sizes it does not take). */
+size_t gq_ffn_i8_workspace_bytes(int64_t T, int64_t H, int64_t I);
+
 /* Diagnostics. */
 const char *gq_last_error(void);       /* message of this thread's last failed call */
 const char *gq_status_str(gq_status s); /* short name of a status */

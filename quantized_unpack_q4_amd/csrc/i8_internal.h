@@ -1,0 +1,67 @@
+// i8_internal.h -- launchers of the 8-bit integer (int8) operators.  Arguments are already
+// validated by i8_api.cpp when these are called: sizes positive, reduction lengths of integer
+// sums at most 131071 (their 8-bit products then sum up in 32 bits), rows of codes a multiple
+// of 16 bytes apart, at most 2^22 (256 rows' byte offsets fit 32 bits), pointers non-null and
+// 16-byte aligned.
+#pragma once
+
+#include "mxfp4_internal.h" // element types
+
+namespace gq {
+
+// Codes [rows][ld], of which K of every row count, and a scale per row.  Every row has the
+// bytes up to the next multiple of 16 behind it; what they hold is not used.
+struct I8Mat {
+    const int8_t *q;
+    int64_t ld;
+    const float *s;
+};
+
+// act(z) = z sigmoid(p(z)): p = z, or the tanh form of GELU.
+constexpr int kSilu = 0, kGelu = 1;
+
+hipError_t launch_quantize_i8(const void *x, int type, int64_t ldx, int8_t *q, int64_t ldq,
+                              float *s, int64_t N, int64_t K, hipStream_t st);
+hipError_t launch_dequant_i8(I8Mat w, void *out, int type, int64_t M, int64_t K, hipStream_t st);
+
+// y[b][r] = sum_k w[r][k] x[b][k] with x quantised per row, 1 <= B <= 16, x and y of `type`.
+hipError_t launch_gemv_i8(I8Mat w, const void *x, void *y, int type, int64_t M, int64_t K, int B,
+                          hipStream_t st);
+// Y[n][r] = sum_k w[r][k] x[n][k].
+hipError_t launch_gemm_i8(I8Mat w, I8Mat x, void *y, int type, int64_t M, int64_t K, int64_t N,
+                          hipStream_t st);
+
+// h[n][i] = act(g) u, g and u the products with gate and up; h dense [N][I] of `type`.
+hipError_t launch_gated_i8(I8Mat gate, I8Mat up, I8Mat x, void *h, int type, int act, int64_t I,
+                           int64_t H, int64_t N, hipStream_t st);
+// The same from 1 to 16 float rows x [N][H], x and h of `type`.
+hipError_t launch_gated_gemv_i8(I8Mat gate, I8Mat up, const void *x, void *h, int type, int act,
+                                int64_t I, int64_t H, int N, hipStream_t st);
+// The gradients of g and u for a gradient dh [N][I] of h: d [N][2][ldd], of dh's 16-bit type.
+hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *dh, uint16_t *d,
+                                 int64_t ldd, int type, int act, int64_t I, int64_t H, int64_t N,
+                                 hipStream_t st);
+
+// dx[n][k] = sum over the parts p and rows m < M of d_p[n][m] w16_p[m][k], w16 each weight
+// rounded to the 16-bit type of d and dx; rows of d are ldd elements apart.
+struct I8GradPart {
+    I8Mat w;
+    const uint16_t *d;
+};
+hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, int64_t ldd, uint16_t *dx, int type,
+                          int64_t M, int64_t K, int64_t N, hipStream_t st);
+
+// The feed-forward block; workspace regions off[]: codes of x, their scales, h, its codes,
+// their scales, total.
+struct I8FfnArgs {
+    I8Mat gate, up, down;
+    const uint16_t *x;
+    uint16_t *out;
+    int type, act;
+    int64_t T, H, I;
+    uint8_t *ws;
+    size_t off[6];
+};
+hipError_t launch_ffn_i8(const I8FfnArgs &a, hipStream_t st);
+
+} // namespace gq

@@ -24,6 +24,8 @@ MAX_BATCH = 16
 GQ_F32 = 0
 GQ_F16 = 1
 GQ_BF16 = 2
+GQ_SILU = 0
+GQ_GELU = 1
 
 EXPORTS = (
     "gq_gemv_q8_0", "gq_gemv_q4k", "gq_gemv_q4k_multi_table_bytes", "gq_gemv_q4k_multi_plan",
@@ -37,7 +39,10 @@ EXPORTS = (
     "gq_moe_workspace_bytes", "gq_moe_workspace_offsets", "gq_dequant_q8_0",
     "gq_dequant_q4k", "gq_quantize_mxfp4", "gq_dequant_mxfp4", "gq_gemv_mxfp4", "gq_gemm_mxfp4",
     "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes",
-    "gq_moe_mxfp4_workspace_offsets", "gq_last_error", "gq_status_str", "gq_version",
+    "gq_moe_mxfp4_workspace_offsets", "gq_quantize_i8", "gq_dequant_i8", "gq_gemv_i8",
+    "gq_gemm_i8", "gq_gemm_i8_backward", "gq_gated_i8", "gq_gated_i8_backward",
+    "gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8", "gq_ffn_i8_workspace_bytes",
+    "gq_last_error", "gq_status_str", "gq_version",
 )
 
 
@@ -137,6 +142,24 @@ def lib() -> ctypes.CDLL:
         L.gq_moe_mxfp4_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
         L.gq_moe_mxfp4_workspace_offsets.restype = st
         L.gq_moe_mxfp4_workspace_offsets.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+        for name, args in (("gq_quantize_i8", [vp, ci, i64, vp, i64, vp, i64, i64, vp]),
+                           ("gq_dequant_i8", [vp, i64, vp, vp, ci, i64, i64, vp]),
+                           ("gq_gemv_i8", [vp, i64, vp, vp, vp, ci, i64, i64, i64, vp]),
+                           ("gq_gemm_i8", [vp, i64, vp] * 2 + [vp, ci, i64, i64, i64, vp]),
+                           ("gq_gemm_i8_backward",
+                            [vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, vp]),
+                           ("gq_gated_i8", [vp, i64, vp] * 3 + [vp, ci, ci, i64, i64, i64, vp]),
+                           ("gq_gated_i8_backward",
+                            [vp, i64, vp] * 3 + [vp, vp, ci, ci, i64, i64, i64, vp, sz, vp]),
+                           ("gq_ffn_i8",
+                            [vp, i64, vp] * 3 + [vp, vp, ci, ci, i64, i64, i64, vp, sz, vp])):
+            f = getattr(L, name)
+            f.restype = st
+            f.argtypes = args
+        for name in ("gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8_workspace_bytes"):
+            f = getattr(L, name)
+            f.restype = sz
+            f.argtypes = [i64, i64, i64]
         L.gq_last_error.restype = ctypes.c_char_p
         L.gq_last_error.argtypes = []
         L.gq_status_str.restype = ctypes.c_char_p
@@ -405,6 +428,69 @@ def gq_moe_gemm_mxfp4(wq_gate, ws_gate, wq_up, ws_up, wq_down, ws_down, x, topk_
                                    _ptr(wq_down), _ptr(ws_down), _ptr(x), _ptr(topk_ids),
                                    _ptr(topk_w), _ptr(out), dtype, T, H, I, E, topk,
                                    int(input_weighted), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+# int8 matrices: codes may be views whose rows are ld bytes apart
+
+def _at(t):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def gq_quantize_i8(x, x_type, ldx, q, ldq, s, N, K, stream=None):
+    """x and q may be strided views: rows ldx elements, ldq bytes apart."""
+    _check(lib().gq_quantize_i8(_at(x), x_type, ldx, _at(q), ldq, _ptr(s), N, K, _stream(stream)))
+
+
+def gq_dequant_i8(q, ldq, s, out, out_type, M, K, stream=None):
+    _check(lib().gq_dequant_i8(_at(q), ldq, _ptr(s), _ptr(out), out_type, M, K, _stream(stream)))
+
+
+def gq_gemv_i8(wq, ldw, ws, x, y, dtype, M, K, B, stream=None):
+    _check(lib().gq_gemv_i8(_at(wq), ldw, _ptr(ws), _ptr(x), _ptr(y), dtype, M, K, B,
+                            _stream(stream)))
+
+
+def gq_gemm_i8(wq, ldw, ws, xq, ldx, xs, y, y_type, M, K, N, stream=None):
+    _check(lib().gq_gemm_i8(_at(wq), ldw, _ptr(ws), _at(xq), ldx, _ptr(xs), _ptr(y), y_type, M, K,
+                            N, _stream(stream)))
+
+
+def gq_gemm_i8_backward(wq, ldw, ws, dy, ldd, dx, dtype, M, K, N, stream=None):
+    _check(lib().gq_gemm_i8_backward(_at(wq), ldw, _ptr(ws), _at(dy), ldd, _ptr(dx), dtype, M, K,
+                                     N, _stream(stream)))
+
+
+def gq_gated_i8(wq_gate, ld_gate, ws_gate, wq_up, ld_up, ws_up, xq, ldx, xs, h, h_type, act, I, H,
+                N, stream=None):
+    _check(lib().gq_gated_i8(_at(wq_gate), ld_gate, _ptr(ws_gate), _at(wq_up), ld_up, _ptr(ws_up),
+                             _at(xq), ldx, _ptr(xs), _ptr(h), h_type, act, I, H, N,
+                             _stream(stream)))
+
+
+def gq_gated_i8_backward_workspace_bytes(N, H, I) -> int:
+    return int(lib().gq_gated_i8_backward_workspace_bytes(N, H, I))
+
+
+def gq_gated_i8_backward(wq_gate, ld_gate, ws_gate, wq_up, ld_up, ws_up, xq, ldx, xs, dh, dx,
+                         dtype, act, I, H, N, ws, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gq_gated_i8_backward(_at(wq_gate), ld_gate, _ptr(ws_gate), _at(wq_up), ld_up,
+                                      _ptr(ws_up), _at(xq), ldx, _ptr(xs), _ptr(dh), _ptr(dx),
+                                      dtype, act, I, H, N, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def gq_ffn_i8_workspace_bytes(T, H, I) -> int:
+    return int(lib().gq_ffn_i8_workspace_bytes(T, H, I))
+
+
+def gq_ffn_i8(wq_gate, ld_gate, ws_gate, wq_up, ld_up, ws_up, wq_down, ld_down, ws_down, x, out,
+              dtype, act, T, H, I, ws, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gq_ffn_i8(_at(wq_gate), ld_gate, _ptr(ws_gate), _at(wq_up), ld_up, _ptr(ws_up),
+                           _at(wq_down), ld_down, _ptr(ws_down), _ptr(x), _ptr(out), dtype, act, T,
+                           H, I, _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def gq_version() -> int:
@@ -704,4 +790,214 @@ def moe_mxfp4(w_gate, w_up, w_down, x, topk_ids, topk_w, ws=None, out=None, stre
                                    _mx_addr("out", o, dev, x.dtype, (T, H)), code, T, H, I, E, topk,
                                    int(input_weighted), _mx_addr("ws", ws, dev, ws.dtype),
                                    ws.numel() * ws.element_size(), _mx_stream(stream, dev)))
+    return o, ws
+
+
+# -- 8-bit integer (int8) matrices: codes int8 [rows][K] whose rows are a multiple of 16 bytes
+# apart (quantize_i8 leaves them so; a view of wider storage), scales float32 [rows] --------
+
+_ACTS = {"silu": GQ_SILU, "gelu": GQ_GELU}
+
+
+def _i8_act(act) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError("unknown activation %r" % (act,))
+    return code
+
+
+def _i8_codes(name, q, dev):
+    """(address, distance of rows in bytes, rows, K) of codes."""
+    if q.get_device() != dev:
+        raise ValueError("%s is on %s, not on the current device" % (name, q.device))
+    if q.dtype != _torch.int8:
+        raise ValueError("%s is %s, expected torch.int8" % (name, q.dtype))
+    if q.dim() != 2:
+        raise ValueError("%s has %d dimensions, expected 2" % (name, q.dim()))
+    rows, K = q.shape
+    if K < 1:
+        raise ValueError("%s has rows of no codes" % name)
+    need = (K + 15) & -16
+    ld, step = q.stride()
+    if rows < 2: # (the stride of a dimension of one is anything)
+        ld = need
+    if (step != 1 and K > 1) or ld < K or ld & 15:
+        raise ValueError("rows of %s must be contiguous and a multiple of 16 bytes apart" % name)
+    if rows and q.storage_offset() + (rows - 1) * ld + need > q.untyped_storage().nbytes():
+        raise ValueError("the storage of %s ends inside the 16 bytes of its last codes" % name)
+    return q.data_ptr(), ld, rows, K
+
+
+def _i8_matrix(name, q, s, dev):
+    """(address of codes, ld, address of scales, rows, K)."""
+    qa, ld, rows, K = _i8_codes(name, q, dev)
+    return qa, ld, _mx_addr(name + " scales", s, dev, _torch.float32, (rows,)), rows, K
+
+
+def _i8_new(rows, K, like, stream):
+    """New codes [rows][K], rows a multiple of 16 bytes apart."""
+    return _mx_new((rows, (K + 15) & -16), _torch.int8, like, stream)[:, :K]
+
+
+def _i8_pair(gate, up, dev):
+    ga, gld, gs, I, H = _i8_matrix("w_gate", *gate, dev)
+    ua, uld, us, I2, H2 = _i8_matrix("w_up", *up, dev)
+    if (I2, H2) != (I, H):
+        raise ValueError("w_up differs from w_gate in shape")
+    return (ga, gld, gs, ua, uld, us), I, H
+
+
+def _rows_2d(name, x):
+    """(rows, K, distance of rows in elements) of a two-dimensional x with contiguous rows."""
+    if x.dim() != 2:
+        raise ValueError("%s has %d dimensions, expected 2" % (name, x.dim()))
+    rows, K = x.shape
+    ld, step = x.stride()
+    if (step != 1 and K > 1) or (rows > 1 and ld < K):
+        raise ValueError("rows of %s must be contiguous and must not overlap" % name)
+    return rows, K, ld if rows > 1 else K
+
+
+def quantize_i8(x, out=None, stream=None):
+    """x [N][K] (float32, float16 or bfloat16; rows contiguous, any distance apart) -> (codes
+    int8 [N][K] with rows a multiple of 16 bytes apart, scales float32 [N]); x may be the
+    weights of a layer (rows are output channels) or its activations (rows are tokens)."""
+    torch, dev = _mx_enter("x", x)
+    code = _mx_dtype(x.dtype)
+    N, K, ldx = _rows_2d("x", x)
+    if out is None:
+        q, s = _i8_new(N, K, x, stream), _mx_new((N,), torch.float32, x, stream)
+    else:
+        q, s = out
+    qa, ldq, sa, rows, KQ = _i8_matrix("codes", q, s, dev)
+    if (rows, KQ) != (N, K):
+        raise ValueError("codes have shape (%d, %d), expected (%d, %d)" % (rows, KQ, N, K))
+    _check(lib().gq_quantize_i8(x.data_ptr(), code, ldx, qa, ldq, sa, N, K,
+                                _mx_stream(stream, dev)))
+    return q, s
+
+
+def dequant_i8(q, s, dtype=None, out=None, stream=None):
+    """The values of codes [M][K] and scales [M] as float32 (or dtype)."""
+    torch, dev = _mx_enter("codes", q)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    qa, ld, sa, M, K = _i8_matrix("codes", q, s, dev)
+    code = _mx_dtype(dtype)
+    if out is None:
+        out = _mx_new((M, K), dtype, q, stream)
+    _check(lib().gq_dequant_i8(qa, ld, sa, _mx_addr("out", out, dev, dtype, (M, K)), code, M, K,
+                               _mx_stream(stream, dev)))
+    return out
+
+
+def gemv_i8(wq, ws, x, out=None, stream=None):
+    """y [B][M] = x [B][K] * W^T in x's dtype (float32, float16 or bfloat16) for int8 W [M][K],
+    1 <= B <= 16, x quantised per row on the way."""
+    _, dev = _mx_enter("x", x)
+    qa, ld, sa, M, K = _i8_matrix("W", wq, ws, dev)
+    code = _mx_dtype(x.dtype)
+    x = _mx_rows("x", x, K)
+    xa = _mx_addr("x", x, dev, x.dtype)
+    B = x.shape[0]
+    y = _mx_new((B, M), x.dtype, x, stream) if out is None else out
+    _check(lib().gq_gemv_i8(qa, ld, sa, xa, _mx_addr("out", y, dev, x.dtype, (B, M)), code, M, K, B,
+                            _mx_stream(stream, dev)))
+    return y
+
+
+def gemm_i8(wq, ws, xq, xs, dtype=None, out=None, stream=None):
+    """Y [N][M] = X * W^T of two int8 matrices, X [N][K] from quantize_i8; Y is float32 unless
+    dtype (or out) says otherwise."""
+    torch, dev = _mx_enter("X codes", xq)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    code = _mx_dtype(dtype)
+    wa, ldw, wsa, M, K = _i8_matrix("W", wq, ws, dev)
+    xa, ldx, xsa, N, KX = _i8_matrix("X", xq, xs, dev)
+    if KX != K:
+        raise ValueError("X has rows of %d codes, W of %d" % (KX, K))
+    y = _mx_new((N, M), dtype, xq, stream) if out is None else out
+    _check(lib().gq_gemm_i8(wa, ldw, wsa, xa, ldx, xsa, _mx_addr("out", y, dev, dtype, (N, M)), code,
+                            M, K, N, _mx_stream(stream, dev)))
+    return y
+
+
+def gemm_i8_backward(wq, ws, dy, out=None, stream=None):
+    """dX [N][K] = dY [N][M] * W in dY's dtype (float16 or bfloat16): the gradient of the values
+    of X for a gradient dY of gemm_i8's (or gemv_i8's) result; rows of dY contiguous, any
+    distance apart."""
+    _, dev = _mx_enter("dY", dy)
+    wa, ldw, wsa, M, K = _i8_matrix("W", wq, ws, dev)
+    code = _mx_dtype(dy.dtype, f32=False)
+    N, MD, ldd = _rows_2d("dY", dy)
+    if MD != M:
+        raise ValueError("dY has rows of %d values, expected %d" % (MD, M))
+    dx = _mx_new((N, K), dy.dtype, dy, stream) if out is None else out
+    _check(lib().gq_gemm_i8_backward(wa, ldw, wsa, dy.data_ptr(), ldd,
+                                     _mx_addr("out", dx, dev, dy.dtype, (N, K)), code, M, K, N,
+                                     _mx_stream(stream, dev)))
+    return dx
+
+
+def gated_i8(w_gate, w_up, xq, xs, act="silu", dtype=None, out=None, stream=None):
+    """h [N][I] = act(X * W_gate^T) * (X * W_up^T), act "silu" or "gelu" (its tanh form); w_gate
+    and w_up pairs (codes [I][H], scales), X [N][H] from quantize_i8; h is float32 unless dtype
+    (or out) says otherwise."""
+    torch, dev = _mx_enter("X codes", xq)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    code, acode = _mx_dtype(dtype), _i8_act(act)
+    pair, I, H = _i8_pair(w_gate, w_up, dev)
+    xa, ldx, xsa, N, HX = _i8_matrix("X", xq, xs, dev)
+    if HX != H:
+        raise ValueError("X has rows of %d codes, W of %d" % (HX, H))
+    h = _mx_new((N, I), dtype, xq, stream) if out is None else out
+    _check(lib().gq_gated_i8(*pair, xa, ldx, xsa, _mx_addr("out", h, dev, dtype, (N, I)), code,
+                             acode, I, H, N, _mx_stream(stream, dev)))
+    return h
+
+
+def gated_i8_backward(w_gate, w_up, xq, xs, dh, act="silu", ws=None, out=None, stream=None):
+    """The gradient of the values of X [N][H] for a gradient dh [N][I] (float16 or bfloat16) of
+    gated_i8's h, in dh's dtype.  Returns (dX, workspace)."""
+    torch, dev = _mx_enter("X codes", xq)
+    pair, I, H = _i8_pair(w_gate, w_up, dev)
+    acode = _i8_act(act)
+    xa, ldx, xsa, N, HX = _i8_matrix("X", xq, xs, dev)
+    if HX != H:
+        raise ValueError("X has rows of %d codes, W of %d" % (HX, H))
+    code = _mx_dtype(dh.dtype, f32=False)
+    da = _mx_addr("dh", dh, dev, dh.dtype, (N, I))
+    if ws is None:
+        need = gq_gated_i8_backward_workspace_bytes(N, H, I)
+        ws = _mx_new((max(need, 16),), torch.uint8, xq, stream)
+    dx = _mx_new((N, H), dh.dtype, xq, stream) if out is None else out
+    _check(lib().gq_gated_i8_backward(*pair, xa, ldx, xsa, da,
+                                      _mx_addr("out", dx, dev, dh.dtype, (N, H)), code, acode, I, H,
+                                      N, _mx_addr("ws", ws, dev, ws.dtype),
+                                      ws.numel() * ws.element_size(), _mx_stream(stream, dev)))
+    return dx, ws
+
+
+def ffn_i8(w_gate, w_up, w_down, x, act="silu", ws=None, out=None, stream=None):
+    """The gated feed-forward block over int8 weights, each a pair (codes, scales): gate and up
+    [I][H], down [H][I]; x [T][H] float16 or bfloat16.  Returns (out [T][H] in x's dtype,
+    workspace)."""
+    torch, dev = _mx_enter("x", x)
+    pair, I, H = _i8_pair(w_gate, w_up, dev)
+    dqa, dld, dsa, H2, I2 = _i8_matrix("w_down", *w_down, dev)
+    if (H2, I2) != (H, I):
+        raise ValueError("w_down is not [H][I]")
+    code, acode = _mx_dtype(x.dtype, f32=False), _i8_act(act)
+    x = _mx_rows("x", x, H)
+    T = x.shape[0]
+    xa = _mx_addr("x", x, dev, x.dtype)
+    if ws is None:
+        need = gq_ffn_i8_workspace_bytes(T, H, I)
+        ws = _mx_new((max(need, 16),), torch.uint8, x, stream)
+    o = _mx_new((T, H), x.dtype, x, stream) if out is None else out
+    _check(lib().gq_ffn_i8(*pair, dqa, dld, dsa, xa, _mx_addr("out", o, dev, x.dtype, (T, H)), code,
+                           acode, T, H, I, _mx_addr("ws", ws, dev, ws.dtype),
+                           ws.numel() * ws.element_size(), _mx_stream(stream, dev)))
     return o, ws
