@@ -24,7 +24,7 @@ PROBE_LIB = os.path.join(PKG, "libgq_probe.so")
 PROBE_SOURCES = ["probes.hip"]
 ARCH = os.environ.get("GQ_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["dequant.hip", "gemv.hip", "gemv_stream.hip", "gemv_mfma.hip", "gemm.hip", "gemm_big.hip", "moe.hip", "moe_skinny.hip", "moe_route.hip", "gemv_q8k.hip", "gemm_q8k.hip", "gemv_q8_0_mfma.hip", "gemv_q4k_f32.hip", "mxfp4_quant.hip", "mxfp4_gemv.hip", "mxfp4_skinny.hip", "mxfp4_tiles.hip", "mxfp4_tiles16.hip", "i8_quant.hip", "i8_products.hip", "gq_api.cpp", "mxfp4_api.cpp", "i8_api.cpp"]
+SOURCES = ["dequant.hip", "gemv.hip", "gemv_stream.hip", "gemv_mfma.hip", "gemm.hip", "gemm_big.hip", "moe.hip", "moe_skinny.hip", "moe_route.hip", "gemv_q8k.hip", "gemm_q8k.hip", "gemv_q8_0_mfma.hip", "gemv_q4k_f32.hip", "mxfp4_quant.hip", "mxfp4_gemv.hip", "mxfp4_skinny.hip", "mxfp4_tiles.hip", "mxfp4_tiles16.hip", "i8_quant.hip", "i8_tiles.hip", "i8_stream.hip", "i8_grad.hip", "gq_api.cpp", "mxfp4_api.cpp", "i8_api.cpp"]
 
 FLAGS = [
     "--offload-arch=" + ARCH,

@@ -248,7 +248,7 @@ gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, co
     GQ_TRY(check_ptr(fn, "dy", dy));
     GQ_TRY(check_ptr(fn, "dx", dx));
     const gq::I8GradPart part{{wq, ldw, ws}, dy};
-    return launched(fn, gq::launch_grad_i8(&part, 1, N > 1 ? ldd : M, dx, type, M, K, N,
+    return launched(fn, gq::launch_grad_i8(&part, 1, false, N > 1 ? ldd : M, dx, type, M, K, N,
                                            (hipStream_t)stream));
 }
 
@@ -306,13 +306,13 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
     GQ_TRY(check_ptr(fn, "dh", dh));
     GQ_TRY(check_ptr(fn, "dx", dx));
     GQ_TRY(check_ws(fn, ws, ws_bytes, need));
-    uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u
+    uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u, times the scales' fractions
     const int64_t ldd = grad_ld(I);
     const gq::I8Mat gate{wq_gate, ld_gate, ws_gate}, upm{wq_up, ld_up, ws_up};
     GQ_TRY(launched(fn, gq::launch_gated_grads_i8(gate, upm, {xq, ldx, xs}, dh, d, ldd, type, act, I,
                                                   H, N, (hipStream_t)stream)));
     const gq::I8GradPart parts[2] = {{gate, d}, {upm, d + ldd}};
-    return launched(fn, gq::launch_grad_i8(parts, 2, 2 * ldd, dx, type, I, H, N,
+    return launched(fn, gq::launch_grad_i8(parts, 2, true, 2 * ldd, dx, type, I, H, N,
                                            (hipStream_t)stream));
 }
 

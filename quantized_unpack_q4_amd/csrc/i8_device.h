@@ -14,30 +14,22 @@
 
 namespace gq {
 
-typedef int int4_t __attribute__((ext_vector_type(4)));
-typedef int int16_t_ __attribute__((ext_vector_type(16)));
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef int int16v __attribute__((ext_vector_type(16)));
 
 // What quantising a row takes: its largest magnitude, the scale (NaN for a row with an
-// infinity or a NaN, whose codes are zero) and the factors of the quotient.  Rows of very
-// small values are held 2^100 times as large, so that 127 / max is finite.
+// infinity or a NaN, whose codes are zero) and the factor of the quotient; r < 0 for rows of
+// very small values, where 127 / max could be infinite: all their codes come from binary64.
 struct I8Row {
-    float top, s, r, f;
+    float top, s, r;
     __device__ __forceinline__ explicit I8Row(uint32_t max_bits)
     {
         const bool bad = max_bits >= 0x7f800000u;
         top = __builtin_bit_cast(float, max_bits);
-        f = top < 0x1p-60f ? 0x1p100f : 1.0f;
         s = bad ? __builtin_nanf("") : top / 127.0f;
-        r = bad || top == 0.0f ? 0.0f : 127.0f / (top * f);
+        r = bad || top == 0.0f ? 0.0f : top < 0x1p-60f ? -1.0f : 127.0f / top;
     }
-    __device__ __forceinline__ int code(float x) const
-    {
-        const float t = x * f * r;
-        float q = rintf(t);
-        if (__builtin_expect(fabsf(t - q) > 0.5f - 0x1p-12f, 0))
-            q = (float)rint(127.0 * (double)x / (double)top);
-        return r == 0.0f ? 0 : (int)q;
-    }
+    __device__ __forceinline__ I8Row(float top_, float s_, float r_) : top(top_), s(s_), r(r_) {}
 };
 
 template <int TYPE>
@@ -109,15 +101,32 @@ struct I8Load8<kF32> {
     __device__ __forceinline__ float value(int j) const { return v[j]; }
 };
 
-// Eight codes of a row, packed.
+// Eight codes of a row, packed.  1.5 * 2^23 added to a quotient leaves the nearest whole number
+// in the low bits, its lowest byte the code.
 template <int TYPE>
 __device__ __forceinline__ uint2 i8_codes8(const I8Load8<TYPE> &v, const I8Row &row)
 {
-    uint32_t t[2] = {0, 0};
+    constexpr float magic = 0x1.8p23f;
+    uint32_t b[8];
+    float off = 0.0f; // largest distance from a whole number
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        t[j >> 2] |= ((uint32_t)row.code(v.value(j)) & 0xffu) << (8 * (j & 3));
-    return make_uint2(t[0], t[1]);
+    for (int j = 0; j < 8; ++j) {
+        const float t = v.value(j) * row.r, m = t + magic;
+        off = fmaxf(off, fabsf(t - (m - magic)));
+        b[j] = __builtin_bit_cast(uint32_t, m);
+    }
+    if (__builtin_expect(off > 0.5f - 0x1p-12f || row.r < 0.0f, 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            b[j] = (uint32_t)(int)rint(127.0 * (double)v.value(j) / (double)row.top);
+    }
+    const uint32_t keep = row.r == 0.0f ? 0u : ~0u; // zero rows, and those with NaN
+    auto pack = [&](int j) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[j + 1], b[j], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[j + 3], b[j + 2], 0x04000c0cu);
+        return (lo | hi) & keep;
+    };
+    return make_uint2(pack(0), pack(4));
 }
 
 // A binary32 value as it stands: without this the compiler may merge its last operation and the
@@ -160,6 +169,41 @@ __device__ __forceinline__ Gate gate_grad(float z, int act)
 __device__ __forceinline__ float i8_scaled(int sum, float ws, float xs)
 {
     return as_is((float)sum * ws * xs);
+}
+
+// A weight row's scale as f times a power of two, f in [1/2, 1): codes times the power of two
+// are exact in both 16-bit types (in binary16 for scales from 2^-25 to 2^8), so that where f
+// can go into the other operand before its rounding, a product rounds one operand only.
+struct ScaleSplit {
+    float f, pow2;
+};
+__device__ __forceinline__ ScaleSplit scale_split(float s)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, s), e = b & 0x7f800000u;
+    if (e == 0 || e >= 0x7f000000u) // zero and subnormal; the last binade, infinity, NaN
+        return {1.0f, s};
+    return {__builtin_bit_cast(float, (b & 0x007fffffu) | 0x3f000000u),
+            __builtin_bit_cast(float, (b & 0xff800000u) + 0x00800000u)};
+}
+
+// Four consecutive 16-bit values from element i (any alignment), of which n exist.
+__device__ __forceinline__ float4_t load4(const uint16_t *x, int64_t i, int64_t n, int type)
+{
+    uint2 u = make_uint2(0, 0);
+    if (n >= 4) {
+        __builtin_memcpy(&u, x + i, 8);
+    } else {
+        if (n > 0)
+            u.x = x[i];
+        if (n > 1)
+            u.x |= (uint32_t)x[i + 1] << 16;
+        if (n > 2)
+            u.y = x[i + 2];
+    }
+    if (type == kBF16)
+        return {__builtin_bit_cast(float, u.x << 16), __builtin_bit_cast(float, u.x & 0xffff0000u),
+                __builtin_bit_cast(float, u.y << 16), __builtin_bit_cast(float, u.y & 0xffff0000u)};
+    return {half_to_float(u.x), half_to_float(u.x >> 16), half_to_float(u.y), half_to_float(u.y >> 16)};
 }
 
 // y[i] = v, rounded to `type`.

@@ -1,0 +1,417 @@
+// i8_tiles.hip -- products of int8 matrices on workgroup tiles.
+//
+// sum_k w[r][k] x[n][k] in whole numbers.  A workgroup of WM x WN waves owns 32 FM WM weight
+// rows by 32 FN WN activation rows; a wave holds FM x FN accumulators of the 32x32x32 product,
+// whose operand is 16 codes (16 bytes) per lane as they lie in memory.  Codes go global -> LDS
+// by direct copies, 128 columns (128 bytes of a row: whole cache lines) per stage, NB stages in
+// turn; operands are read a step ahead of the products, copies are issued between them.
+//
+// Gate/up: half of a tile's weight rows are rows of the gate matrix, half the same rows of the
+// up matrix, and a wave holds both of a row: h, or the gradients of g and u, is formed in
+// registers.
+//
+// The last stage of a K that is no multiple of 128: copies past a row's last 16 bytes repeat
+// those, and the weights' codes past K are zeroed in registers (what lies there in the
+// activations then counts nothing).
+#include <algorithm>
+#include <type_traits>
+
+#include "gq_internal.h"
+#include "gq_lds_dma.h"
+#include "i8_device.h"
+#include "mxfp4_tile.h"
+
+namespace gq {
+
+namespace {
+
+enum { kPlain = 0, kGated = 1, kGrads = 2 };
+
+struct I8TileArgs {
+    I8Mat w, w2; // gate/up: gate, up
+    I8Mat x;
+    void *y;
+    const uint16_t *dh; // kGrads
+    int64_t ldy;        // elements between rows of y
+    int64_t part;       // kGrads: elements from the gradient of g to that of u
+    int type, act;
+    int M, K, N; // M rows of each matrix
+    int tiles_m, tiles_total, tiles_whole;
+};
+
+__device__ __forceinline__ int16v mfma_i8(uint4 a, uint4 b, int16v c)
+{
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(int4v, a),
+                                                 __builtin_bit_cast(int4v, b), c, 0, 0, 0);
+}
+
+// An address that is the same in all lanes, for scalar registers.
+__device__ __forceinline__ const int8_t *uniform(const int8_t *p)
+{
+    const uint64_t a = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    return (const int8_t *)((uint64_t)hi << 32 | lo);
+}
+
+template <int WM, int WN, int FM, int FN, int NB>
+constexpr int i8_lds_bytes()
+{
+    return std::max(NB * (32 * FM * WM + 32 * FN * WN) * 128, WM * WN * store_scratch(4 * FM, 4));
+}
+
+// The scales of weight rows m .. m + 3, of which those below M exist.
+__device__ __forceinline__ float4_t scales4(const float *s, int64_t m, int64_t M)
+{
+    if (m + 4 <= M)
+        return *reinterpret_cast<const float4_t *>(s + m);
+    float4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (m + i < M)
+            v[i] = s[m + i];
+    return v;
+}
+
+// The tile of weight rows m0 .. (of each matrix) and activation rows n0 ..: NB stages in LDS,
+// of which NB - 1 are in flight when a stage begins.
+template <int MODE, int WM, int WN, int FM, int FN, int NB, bool TAIL>
+__device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uint8_t *lds)
+{
+    constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN, BR = BM + BN;
+    constexpr int NC = BR / 8 / NW; // 1 KB copies per wave and stage
+    constexpr bool PAIR = MODE != kPlain;
+    constexpr int BW = PAIR ? BM / 2 : BM, FW = PAIR ? FM / 2 : FM; // rows, fragments of a matrix
+    // one wave a SIMD: the compiler keeps the accumulators in the other register file
+    constexpr bool AGPR = NW <= 4 && i8_lds_bytes<WM, WN, FM, FN, NB>() > (80 << 10);
+    static_assert(NC * 8 * NW == BR && BW % 8 == 0 && (!PAIR || FM % 2 == 0), "whole copies, pairs");
+    const int M = p.M, K = p.K;
+    const uint32_t ldw = (uint32_t)p.w.ld, ldw2 = (uint32_t)(PAIR ? p.w2.ld : p.w.ld), ldx = (uint32_t)p.x.ld;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int r = lane & 31, h = lane >> 5;
+    const int mv = min(M - m0, BW), nv = min(p.N - n0, BN); // valid rows
+    const int nch = (K + 15) >> 4, nst = (nch + 7) >> 3;     // chunks of 16 codes, stages
+    const int8_t *aq = p.w.q + (int64_t)m0 * p.w.ld;
+    const int8_t *aq2 = PAIR ? p.w2.q + (int64_t)m0 * p.w2.ld : aq;
+    const int8_t *bq = p.x.q + (int64_t)n0 * p.x.ld;
+
+    // what belongs to the matrix of a tile row: gate, up, activations
+    auto pick = [](int row, auto gate, auto up, auto x) {
+        return row >= BM ? x : PAIR && row >= BW ? up : gate;
+    };
+    // copy i of this wave: tile rows 8 (NC wave + i) + lane / 8 (weight rows first),
+    // slot lane % 8; the 8 rows are of one matrix
+    uint32_t off[NC], chk[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int row = 8 * (NC * wave + i) + (lane >> 3);
+        const int rr = row < BM ? min(PAIR && row >= BW ? row - BW : row, mv - 1) : min(row - BM, nv - 1);
+        const int row0 = 8 * (NC * wave + i);
+        off[i] = (uint32_t)rr * pick(row0, ldw, ldw2, ldx);
+        chk[i] = (lane & 7) ^ swz8(row);
+    }
+    const uint32_t base = lds_addr(lds);
+    // Past the last stage the copies repeat it into the buffer whose turn it is, which no one
+    // reads.
+    auto copy1 = [&](int st, int i) {
+        const int src = min(st, nst - 1);
+        const uint32_t last = (uint32_t)(nch - 1 - 8 * src); // chunks past it repeat it
+        const int row0 = 8 * (NC * wave + i);
+        load_lds16(uniform(pick(row0, aq, aq2, bq) + (int64_t)src * 128), off[i] + 16u * (TAIL ? min(chk[i], last) : chk[i]),
+                   __builtin_amdgcn_readfirstlane(base + (st % NB * BR + row0) * 128));
+    };
+
+    int16v acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = int16v{};
+
+    struct Frag {
+        uint4 a[FM], b[FN];
+    };
+    // operand addresses: the swizzle of row 32 i + r is that of r
+    uint32_t rof[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        rof[t] = r * 128 + 16 * ((2 * t + h) ^ swz8(r));
+    // first tile row of fragment i of this wave
+    auto frow = [&](int i) { return i < FW ? 32 * (FW * wm + i) : BW + 32 * (FW * wm + i - FW); };
+    const int brow = (BM + 32 * FN * wn) * 128;
+    auto read = [&](int st, int t, Frag &f) {
+        const uint8_t *S = lds + st % NB * BR * 128 + rof[t];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            f.a[i] = ld16(S + frow(i) * 128);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            f.b[j] = ld16(S + brow + 32 * j * 128);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // the products of step t of stage st; copies c0 .. c0 + CP - 1 of stage stc (uniform)
+    // are issued between them
+    constexpr int CP = (NC + 1) / 2, EV = FM * FN / CP > 0 ? FM * FN / CP : 1;
+    auto multiply = [&](int st, auto tc, Frag &f, int stc, int c0) {
+        constexpr int t = decltype(tc)::value;
+        if constexpr (TAIL) {
+            if (st == nst - 1) { // codes past K are zero
+                const int left = K - (128 * st + 16 * (2 * t + h));
+                uint32_t mask[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int n = min(max(left - 4 * u, 0), 4);
+                    mask[u] = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    f.a[i].x &= mask[0], f.a[i].y &= mask[1], f.a[i].z &= mask[2], f.a[i].w &= mask[3];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                acc[i][j] = mfma_i8(f.a[i], f.b[j], acc[i][j]);
+                // the products stay where they are written, between reads and copies
+                if constexpr (AGPR)
+                    asm volatile("" : "+a"(acc[i][j]));
+                else
+                    asm volatile("" : "+v"(acc[i][j]));
+                const int u = i * FN + j;
+                if (c0 >= 0 && u % EV == EV - 1 && u / EV < CP && c0 + u / EV < NC)
+                    copy1(stc, c0 + u / EV);
+            }
+        if (c0 >= 0)
+#pragma unroll
+            for (int u = FM * FN / EV; u < CP; ++u)
+                if (c0 + u < NC)
+                    copy1(stc, c0 + u);
+    };
+
+#pragma unroll
+    for (int g = 0; g < NB - 1; ++g)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            copy1(g, i);
+    wait_copies<(NB - 2) * NC>();
+    Frag f0, f1;
+    read(0, 0, f0);
+#pragma unroll
+    for (int i = 0; i < CP; ++i)
+        copy1(NB - 1, i);
+    for (int st = 0; st < nst; ++st) {
+        read(st, 1, f1);
+        multiply(st, std::integral_constant<int, 0>{}, f0, st + NB - 1, CP);
+        read(st, 2, f0);
+        multiply(st, std::integral_constant<int, 1>{}, f1, 0, -1);
+        read(st, 3, f1);
+        multiply(st, std::integral_constant<int, 2>{}, f0, 0, -1);
+        // the next stage's copies have landed and every wave has read this stage,
+        // whose place the one after takes
+        wait_copies<(NB - 2) * NC>();
+        read(st + 1, 0, f0); // (after the last stage: read and not used)
+        multiply(st, std::integral_constant<int, 3>{}, f1, st + NB, 0);
+    }
+    wait_copies<0>();
+
+    // element v of an accumulator: weight row 8 (v / 4) + 4 h + v % 4, activation row r
+    const int64_t m = m0 + 32 * FW * wm;
+    if (m >= M)
+        return;
+    uint8_t *scr = lds + wave * store_scratch(4 * FM, 4);
+    auto scaled4 = [&](int i, int j, int v4, float4_t ws, float xs) {
+        float4_t v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[c] = i8_scaled(acc[i][j][4 * v4 + c], ws[c], xs);
+        return v;
+    };
+    // weight rows of a store: all of the wave's, or a fragment's where two results are held
+    constexpr int G = MODE == kGrads ? 4 : 4 * FW;
+    auto store = [&](const float4_t(&v)[G], void *y, int64_t n, int left, int64_t m) {
+        if (p.type == kF32)
+            store_rows<kF32>(scr, y, n, left, m, M, v, p.ldy);
+        else if (p.type == kF16)
+            store_rows<kF16>(scr, y, n, left, m, M, v, p.ldy);
+        else
+            store_rows<kBF16>(scr, y, n, left, m, M, v, p.ldy);
+    };
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int n = 32 * (FN * wn + j);
+        if (n >= nv)
+            break;
+        const int64_t nr = n0 + min(n + r, nv - 1);
+        const float xs = p.x.s[nr];
+        float4_t v[G], v2[MODE == kGrads ? G : 1];
+#pragma unroll
+        for (int i = 0; i < FW; ++i) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+                const int64_t mr = m + 32 * i + 8 * v4 + 4 * h;
+                const float4_t ws = scales4(p.w.s, mr, M);
+                const float4_t g = scaled4(i, j, v4, ws, xs);
+                if constexpr (MODE == kPlain) {
+                    v[4 * i + v4] = g;
+                } else {
+                    const float4_t us = scales4(p.w2.s, mr, M);
+                    const float4_t u = scaled4(FW + i, j, v4, us, xs);
+                    if constexpr (MODE == kGated) {
+                        v[4 * i + v4] = float4_t{gated_value(g[0], u[0], p.act), gated_value(g[1], u[1], p.act),
+                                                 gated_value(g[2], u[2], p.act), gated_value(g[3], u[3], p.act)};
+                    } else {
+                        const float4_t d = load4(p.dh, nr * M + mr, M - mr, p.type);
+                        float4_t dg, du;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const Gate a = gate_grad(g[c], p.act);
+                            dg[c] = d[c] * u[c] * a.da * scale_split(ws[c]).f;
+                            du[c] = d[c] * a.a * scale_split(us[c]).f;
+                        }
+                        v[v4] = dg;
+                        v2[v4] = du;
+                    }
+                }
+            }
+            if constexpr (MODE == kGrads) {
+                if (m + 32 * i < M) {
+                    store(v, p.y, n0 + n, nv - n, m + 32 * i);
+                    store(v2, reinterpret_cast<uint16_t *>(p.y) + p.part, n0 + n, nv - n, m + 32 * i);
+                }
+            }
+        }
+        if constexpr (MODE != kGrads)
+            store(v, p.y, n0 + n, nv - n, m);
+    }
+}
+
+// Whether a launch of these tiles may cut its last ones: the 256-row ones.
+constexpr bool cuts(int FM) { return FM == 4; }
+
+template <int MODE, int WM, int WN, int FM, int FN, int NB, bool TAIL>
+__global__ __launch_bounds__(64 * WM * WN, 2) void i8_tile_kernel(I8TileArgs p)
+{
+    constexpr int BM = 32 * FM * WM / (MODE == kPlain ? 1 : 2), BN = 32 * FN * WN;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(
+        i8_lds_bytes<WM, WN, FM, FN, NB>(),
+        cuts(FM) ? i8_lds_bytes<WM, WN, FM, FN / 2, NB + 1>() : 0)]; // (halves: one stage more)
+    const TileWork work = tile_work(p.tiles_total, p.tiles_whole);
+    if (work.tile < 0)
+        return;
+    int tm, tn;
+    tile_pos(work.tile, p.tiles_m, p.tiles_total / p.tiles_m, tm, tn);
+    if constexpr (cuts(FM)) {
+        if (work.half >= 0) {
+            const int n0 = tn * BN + work.half * (BN / 2);
+            if (n0 < p.N)
+                i8_tile<MODE, WM, WN, FM, FN / 2, NB + 1, TAIL>(p, tm * BM, n0, lds);
+            return;
+        }
+    }
+    i8_tile<MODE, WM, WN, FM, FN, NB, TAIL>(p, tm * BM, tn * BN, lds);
+}
+
+template <int MODE, int WM, int WN, int FM, int FN, int NB>
+hipError_t launch_tiles(I8TileArgs p, hipStream_t st)
+{
+    constexpr int BM = 32 * FM * WM / (MODE == kPlain ? 1 : 2), BN = 32 * FN * WN;
+    p.tiles_m = (p.M + BM - 1) / BM;
+    p.tiles_total = p.tiles_m * ((p.N + BN - 1) / BN);
+    p.tiles_whole = cuts(FM) ? tiles_whole(p.tiles_total, device_cus()) : p.tiles_total;
+    const dim3 grid(tile_grid(p.tiles_total, p.tiles_whole)), block(64 * WM * WN);
+    if (p.K % 128 == 0)
+        hipLaunchKernelGGL((i8_tile_kernel<MODE, WM, WN, FM, FN, NB, false>), grid, block, 0, st, p);
+    else
+        hipLaunchKernelGGL((i8_tile_kernel<MODE, WM, WN, FM, FN, NB, true>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+// The tile for a shape, from an estimate of the time of a stage (128 columns): full rounds of
+// tiles on the device, and a last one by how many CUs it has.
+int tile_choice(int64_t M, int64_t N)
+{
+    const int64_t cus = device_cus();
+    auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b); };
+    auto last = [&](int64_t rest, double lone, double full) {
+        return rest ? lone + (full - lone) * (double)rest / (double)cus : 0;
+    };
+    const int64_t t1 = tiles(64), t2 = tiles(128), t3 = tiles(256), whole = tiles_whole(t3, cus);
+    const double t64 = 0.39 + 0.36 * std::max(0.0, (double)t1 / (double)cus - 1.0);
+    const double t128 = 0.75 * (double)(t2 / cus) + last(t2 % cus, 0.63, 0.78);
+    const double t256 = 2.1 * (double)(t3 / cus) +
+                        (whole < t3 ? last(2 * (t3 - whole), 1.02, 1.22) : last(t3 % cus, 1.5, 2.1));
+    return t64 <= t128 && t64 <= t256 ? 64 : t128 <= t256 ? 128 : 256;
+}
+
+template <int MODE>
+hipError_t launch_pair(const I8TileArgs &p, hipStream_t st)
+{
+    switch (tile_choice(2 * (int64_t)p.M, p.N)) {
+    case 64: return launch_tiles<MODE, 2, 2, 2, 1, 3>(p, st);
+    case 128: return launch_tiles<MODE, 2, 2, 2, 2, 3>(p, st);
+    default: return launch_tiles<MODE, 2, 4, 4, 2, 2>(p, st);
+    }
+}
+
+} // namespace
+
+hipError_t launch_i8_tiles(I8Mat w, I8Mat x, void *y, int type, int64_t M, int64_t K, int64_t N,
+                           hipStream_t st)
+{
+    I8TileArgs p{};
+    p.w = w;
+    p.x = x;
+    p.y = y;
+    p.ldy = M;
+    p.type = type;
+    p.M = (int)M;
+    p.K = (int)K;
+    p.N = (int)N;
+    switch (tile_choice(M, N)) {
+    case 64: return launch_tiles<kPlain, 2, 2, 1, 1, 4>(p, st);
+    case 128: return launch_tiles<kPlain, 2, 2, 2, 2, 3>(p, st);
+    default: return launch_tiles<kPlain, 2, 4, 4, 2, 2>(p, st);
+    }
+}
+
+hipError_t launch_gated_tiles(I8Mat gate, I8Mat up, I8Mat x, void *h, int type, int act, int64_t I,
+                              int64_t H, int64_t N, hipStream_t st)
+{
+    I8TileArgs p{};
+    p.w = gate;
+    p.w2 = up;
+    p.x = x;
+    p.y = h;
+    p.ldy = I;
+    p.type = type;
+    p.act = act;
+    p.M = (int)I;
+    p.K = (int)H;
+    p.N = (int)N;
+    return launch_pair<kGated>(p, st);
+}
+
+hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *dh, uint16_t *d,
+                                 int64_t ldd, int type, int act, int64_t I, int64_t H, int64_t N,
+                                 hipStream_t st)
+{
+    I8TileArgs p{};
+    p.w = gate;
+    p.w2 = up;
+    p.x = x;
+    p.y = d;
+    p.dh = dh;
+    p.ldy = 2 * ldd;
+    p.part = ldd;
+    p.type = type;
+    p.act = act;
+    p.M = (int)I;
+    p.K = (int)H;
+    p.N = (int)N;
+    return launch_pair<kGrads>(p, st);
+}
+
+} // namespace gq

@@ -71,11 +71,11 @@ constexpr int store_scratch(int G, int esize) { return 32 * (8 * G * esize + 16)
 // holds v[g] = weight rows 8 g + 4 h + 0..3 of activation row r.  The values go through
 // LDS (rows padded by 16 bytes), so that a row leaves as whole runs of 16 G (32 G)
 // bytes instead of 16-byte pieces of 32 rows; on 256 x 256 tiles of 4096 columns that
-// takes a tenth off the whole product.  y at (activation row n, weight row m), nv
-// activation rows and mleft weight rows exist.
+// takes a tenth off the whole product.  y at (activation row n, weight row m), its rows ld
+// elements apart (M where not given); nv activation rows and M - m weight rows exist.
 template <int TYPE, int G>
 __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int nv, int64_t m,
-                                           int64_t M, const float4_t (&v)[G])
+                                           int64_t M, const float4_t (&v)[G], int64_t ld)
 {
     constexpr int ES = TYPE == kF32 ? 4 : 2, ST = 8 * G * ES + 16, CE = 16 / ES;
     constexpr int CPR = 8 * G / CE; // 16-byte chunks of a row
@@ -90,7 +90,7 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
                                                        mx_pack2<TYPE == kBF16>(v[g][2], v[g][3]));
     }
     lds_wave_order();
-    const bool vec = M % CE == 0; // rows start 16-byte aligned
+    const bool vec = ld % CE == 0; // rows start 16-byte aligned
     const int64_t mleft = M - m;
 #pragma unroll
     for (int k = 0; k < 32 * CPR / 64; ++k) {
@@ -98,8 +98,8 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
         if (row >= nv || col >= mleft)
             continue;
         const uint8_t *s = scr + row * ST + col * ES;
-        uint8_t *d = reinterpret_cast<uint8_t *>(y) + ((n + row) * M + m + col) * ES;
-        if (vec) { // whole chunks exist: mleft is a multiple of CE too
+        uint8_t *d = reinterpret_cast<uint8_t *>(y) + ((n + row) * ld + m + col) * ES;
+        if (vec && col + CE <= mleft) {
             *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(s);
         } else {
 #pragma unroll
@@ -113,6 +113,12 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
         }
     }
     lds_wave_order();
+}
+template <int TYPE, int G>
+__device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int nv, int64_t m,
+                                           int64_t M, const float4_t (&v)[G])
+{
+    store_rows<TYPE, G>(scr, y, n, nv, m, M, v, M);
 }
 
 } // namespace gq

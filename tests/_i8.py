@@ -49,6 +49,12 @@ def weights16(wq, ws, t):
         return round_to(wq.astype(F) * ws[:, None], t)
 
 
+def split_scales(s):
+    """s = f 2^e with 1/2 <= f < 1: (f, 2^e) in binary64."""
+    f, e = np.frexp(s.astype(np.float64))
+    return f, np.exp2(e)
+
+
 def act(z, kind):
     """(act(z), act'(z), p(z)) in binary64."""
     z = np.asarray(z, np.float64)

@@ -297,8 +297,8 @@ def test_gated_far_arguments(kind):
         assert np.isfinite(values(dx)).all()
         want = da[0, i] * zz[0, i] + a[0, i]
         size = abs(da[0, i] * zz[0, i]) + abs(a[0, i])
-        # dg, du and the weight rounded to bfloat16 each, and the result
-        assert abs(values(dx)[0, 0] - want) <= size * 4 * 2.0 ** -8 + 1e-6, (z[i], values(dx)[0, 0], want)
+        # dg and du rounded to bfloat16 each, and the result
+        assert abs(values(dx)[0, 0] - want) <= size * 2.1 * 2.0 ** -8 + 1e-6, (z[i], values(dx)[0, 0], want)
 
 
 # -- gradients -----------------------------------------------------------------
@@ -371,15 +371,18 @@ def test_gated_backward(I, H, N, t, kind):
     xq, xs = i8.rows(32, N, H)
     dh, d64 = floats(46, N, I, t)
     g, u, (a, da, p) = gated_reference(gate, up, xq, xs, kind)
-    wg, wu = i8.weights16(*gate, t), i8.weights16(*up, t)
     dg, du = d64 * u * da, d64 * a
-    want = dg @ wg + du @ wu
     # act' = sig + z p' sig (1 - sig): the errors of its two terms, each relative
     sig = np.where(g != 0, a / np.where(g != 0, g, 1), 0.5)
     terms = np.abs(sig) + np.abs(da - sig) * 2
     eg = np.abs(d64 * u) * terms * (2 * i8.act_rel(p) + 8 * 2.0 ** -24) + 2.0 ** -120
     eu = np.abs(du) * i8.act_rel(p) + 2.0 ** -120
+    # operands: the gradients times the scales' fractions, rounded; codes times powers of two
+    (fg, pg), (fu, pu) = i8.split_scales(gate[1]), i8.split_scales(up[1])
+    wg, wu = gate[0] * pg[:, None], up[0] * pu[:, None]
+    dg, du, eg, eu = dg * fg, du * fu, eg * fg, eu * fu
     eg, eu = eg + i8.half_step(np.abs(dg) + eg, t), eu + i8.half_step(np.abs(du) + eu, t)
+    want = dg @ wg + du @ wu
     size = (np.abs(dg) + eg) @ np.abs(wg) + (np.abs(du) + eu) @ np.abs(wu)
     tol = eg @ np.abs(wg) + eu @ np.abs(wu) + grad_tolerance(size, 2 * I, want, t)
     dx, _ = gq.gated_i8_backward(matrix(*gate, extra=1), matrix(*up), *matrix(xq, xs), dh, act=kind)
@@ -404,15 +407,15 @@ def test_gated_gradient_against_differences(kind):
 
     g = np.random.default_rng(54)
     a, da, _ = i8.act(x @ wg.T, kind)
-    # dg, du, the weights and the result are each rounded to 16 bits: 3 half steps of every term
-    # and one of the result, along v
+    # dg, du and the result are each rounded to 16 bits: a half step of every term and one of
+    # the result, along v (and their binary32 errors, far smaller)
     size = np.abs(d64 * (x @ wu.T) * da) @ np.abs(wg) + np.abs(d64 * a) @ np.abs(wu)
     for _ in range(5):
         v = g.standard_normal((N, H))
         eps = 1e-5
         diff = (loss(x + eps * v) - loss(x - eps * v)) / (2 * eps)
         got = (values(dx) * v).sum(-1)
-        tol = (size * np.abs(v)).sum(-1) * 4 * EPS2["f16"] + 1e-6 * np.abs(diff)
+        tol = (size * np.abs(v)).sum(-1) * 2.5 * EPS2["f16"] + 1e-6 * np.abs(diff)
         assert (np.abs(got - diff) <= tol).all(), (got, diff, tol)
 
 
