@@ -562,14 +562,21 @@ gq_status gq_quantize_i8(const void *x, int x_type, int64_t ldx, int8_t *q, int6
 gq_status gq_dequant_i8(const int8_t *q, int64_t ldq, const float *s, void *out, int out_type,
                         int64_t M, int64_t K, void *stream);
 
-/* int8 matrix-vector product for 1 <= B <= GQ_GEMV_MAX_BATCH activation rows, each quantised
- * on the way as by gq_quantize_i8 (the same results as that and gq_gemm_i8, bit for bit, in
- * one launch):
+/* int8 matrix-vector product for 1 <= B <= GQ_GEMV_MAX_BATCH activation rows, quantised on the
+ * way as by gq_quantize_i8 (the same results as that and gq_gemm_i8, bit for bit):
  *   y[b][r] = sum_k w[r][k] * v(x)[b][k].
+ * Few values (B*K <= 16384) are quantised by the workgroups that multiply them, in one launch
+ * and without a workspace (wsp may be NULL); more are quantised once, by a launch before, into
+ * wsp: at least gq_gemv_i8_workspace_bytes(K, B) bytes, 16-byte aligned, contents on entry
+ * ignored; not to be in use by another call while this one runs.
  * x: [B][K] and y: [B][M], both of `type` (any gq_dtype).  Requires K <= 131071, M <= 2^26,
  * ldw <= 2^22. */
 gq_status gq_gemv_i8(const int8_t *wq, int64_t ldw, const float *ws, const void *x, void *y,
-                     int type, int64_t M, int64_t K, int64_t B, void *stream);
+                     int type, int64_t M, int64_t K, int64_t B, void *wsp, size_t ws_bytes,
+                     void *stream);
+/* Its workspace size: 0 where it needs none (and, with the reason in gq_last_error(), for sizes
+ * it does not take). */
+size_t gq_gemv_i8_workspace_bytes(int64_t K, int64_t B);
 
 /* The product of two int8 matrices on the int8 matrix cores, any number of activation rows:
  *   Y[n][r] = xs[n] ws[r] sum_k xq[n][k] wq[r][k].

@@ -81,18 +81,27 @@ gq_status product_sizes(const char *fn, const char *m, int64_t M, const char *k,
     return check_most(fn, "the number of outputs", M * N, kMaxOutputs);
 }
 
-gq_status check_ws(const char *fn, const void *ws, size_t have, size_t need)
+gq_status check_ws(const char *fn, const char *name, const void *ws, size_t have, size_t need)
 {
     if (!ws)
-        return fail(GQ_EWORKSPACE, "%s: ws is NULL (needs %zu bytes)", fn, need);
+        return fail(GQ_EWORKSPACE, "%s: %s is NULL (needs %zu bytes)", fn, name, need);
     if (!aligned16(ws))
-        return fail(GQ_EALIGN, "%s: ws (%p) is not 16-byte aligned", fn, ws);
+        return fail(GQ_EALIGN, "%s: %s (%p) is not 16-byte aligned", fn, name, ws);
     if (have < need)
         return fail(GQ_EWORKSPACE, "%s: ws_bytes = %zu is below the required %zu", fn, have, need);
     return GQ_OK;
 }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// The workspace of the matrix-vector product: codes, scales, total (zero where it takes none).
+void gemv_layout(int64_t K, int64_t B, size_t off[3])
+{
+    const bool fused = B == 0 || gq::i8_fused(K, B);
+    off[0] = 0;
+    off[1] = fused ? 0 : up((size_t)(B * up16(K)));
+    off[2] = fused ? 0 : up(off[1] + (size_t)B * 4);
+}
 
 // The sizes the feed-forward block takes, and its workspace's regions.
 gq_status ffn_shape(const char *fn, int64_t T, int64_t H, int64_t I, size_t off[6])
@@ -190,7 +199,8 @@ gq_status gq_dequant_i8(const int8_t *q, int64_t ldq, const float *s, void *out,
 }
 
 gq_status gq_gemv_i8(const int8_t *wq, int64_t ldw, const float *ws, const void *x, void *y,
-                     int type, int64_t M, int64_t K, int64_t B, void *stream)
+                     int type, int64_t M, int64_t K, int64_t B, void *wsp, size_t ws_bytes,
+                     void *stream)
 {
     static const char fn[] = "gq_gemv_i8";
     GQ_TRY(check_type(fn, "type", type, true));
@@ -204,8 +214,33 @@ gq_status gq_gemv_i8(const int8_t *wq, int64_t ldw, const float *ws, const void 
     GQ_TRY(check_matrix(fn, "wq", wq, "ws", ws));
     GQ_TRY(check_ptr(fn, "x", x));
     GQ_TRY(check_ptr(fn, "y", y));
-    return launched(fn, gq::launch_gemv_i8({wq, ldw, ws}, x, y, type, M, K, (int)B,
+    size_t off[3];
+    gemv_layout(K, B, off);
+    if (off[2] == 0)
+        return launched(fn, gq::launch_gemv_i8({wq, ldw, ws}, x, y, type, M, K, (int)B,
+                                               (hipStream_t)stream));
+    GQ_TRY(check_ws(fn, "wsp", wsp, ws_bytes, off[2]));
+    int8_t *xq = (int8_t *)wsp;
+    float *xs = (float *)((char *)wsp + off[1]);
+    GQ_TRY(launched(fn, gq::launch_quantize_i8(x, type, K, xq, up16(K), xs, B, K,
+                                               (hipStream_t)stream)));
+    return launched(fn, gq::launch_gemm_i8({wq, ldw, ws}, {xq, up16(K), xs}, y, type, M, K, B,
                                            (hipStream_t)stream));
+}
+
+size_t gq_gemv_i8_workspace_bytes(int64_t K, int64_t B)
+{
+    static const char fn[] = "gq_gemv_i8_workspace_bytes";
+    size_t off[3] = {};
+    auto shape = [&] {
+        if (B < 0 || B > GQ_GEMV_MAX_BATCH)
+            return fail(GQ_EINVAL, "%s: B = %lld is outside [0, %d]", fn, (long long)B,
+                        GQ_GEMV_MAX_BATCH);
+        GQ_TRY(check_size(fn, "K", K, kMaxK, false));
+        gemv_layout(K, B, off);
+        return GQ_OK;
+    };
+    return quietly(shape, &off[2]);
 }
 
 gq_status gq_gemm_i8(const int8_t *wq, int64_t ldw, const float *ws, const int8_t *xq, int64_t ldx,
@@ -305,7 +340,7 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
     GQ_TRY(check_matrix(fn, "xq", xq, "xs", xs));
     GQ_TRY(check_ptr(fn, "dh", dh));
     GQ_TRY(check_ptr(fn, "dx", dx));
-    GQ_TRY(check_ws(fn, ws, ws_bytes, need));
+    GQ_TRY(check_ws(fn, "ws", ws, ws_bytes, need));
     uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u, times the scales' fractions
     const int64_t ldd = grad_ld(I);
     const gq::I8Mat gate{wq_gate, ld_gate, ws_gate}, upm{wq_up, ld_up, ws_up};
@@ -343,7 +378,7 @@ gq_status gq_ffn_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate
     GQ_TRY(check_matrix(fn, "wq_down", wq_down, "ws_down", ws_down));
     GQ_TRY(check_ptr(fn, "x", x));
     GQ_TRY(check_ptr(fn, "out", out));
-    GQ_TRY(check_ws(fn, ws, ws_bytes, a.off[5]));
+    GQ_TRY(check_ws(fn, "ws", ws, ws_bytes, a.off[5]));
     a.gate = {wq_gate, ld_gate, ws_gate};
     a.up = {wq_up, ld_up, ws_up};
     a.down = {wq_down, ld_down, ws_down};

@@ -24,6 +24,9 @@ hipError_t launch_quantize_i8(const void *x, int type, int64_t ldx, int8_t *q, i
                               float *s, int64_t N, int64_t K, hipStream_t st);
 hipError_t launch_dequant_i8(I8Mat w, void *out, int type, int64_t M, int64_t K, hipStream_t st);
 
+// Whether B rows of K floats are quantised by the workgroups that multiply them; the next two
+// take no others.
+bool i8_fused(int64_t K, int64_t B);
 // y[b][r] = sum_k w[r][k] x[b][k] with x quantised per row, 1 <= B <= 16, x and y of `type`.
 hipError_t launch_gemv_i8(I8Mat w, const void *x, void *y, int type, int64_t M, int64_t K, int B,
                           hipStream_t st);

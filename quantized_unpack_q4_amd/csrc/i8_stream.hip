@@ -7,9 +7,8 @@
 //
 // Activations are codes, read from memory in the same form, or floats, which every workgroup
 // quantises itself: the largest magnitude of each row over all waves, then each wave the codes
-// of its own run into LDS, all at once where they fit (one quantisation for all of a
-// workgroup's tiles), else in pieces.  Columns past K get zero codes, so that what lies there
-// in the weights counts nothing.
+// of its own run into LDS, once for all of a workgroup's tiles.  Columns past K get zero codes,
+// so that what lies there in the weights counts nothing.
 #include <algorithm>
 
 #include "gq_internal.h"
@@ -28,8 +27,7 @@ struct I8StreamArgs {
     void *y;
     int type, act;
     int M, K, B;
-    int run;   // columns of a wave, a multiple of 64
-    int piece; // columns quantised at once, a power of two
+    int run; // columns of a wave, a multiple of 64
 };
 
 __device__ __forceinline__ int4v mfma16_i8(uint4 a, uint4 b, int4v c)
@@ -38,9 +36,9 @@ __device__ __forceinline__ int4v mfma16_i8(uint4 a, uint4 b, int4v c)
                                                  __builtin_bit_cast(int4v, b), c, 0, 0, 0);
 }
 
-// Bytes of LDS for codes: rows of a piece are 16 bytes further apart than the piece is long,
-// so that 16 rows' reads touch distinct banks.
-constexpr int codes_bytes(int W, int B, int piece) { return W * B * (piece + 16); }
+// Bytes of LDS for codes: rows of a run are 16 bytes further apart than the run is long, so
+// that 16 rows' reads touch distinct banks.
+constexpr int64_t codes_bytes(int W, int64_t B, int64_t run) { return W * B * (run + 16); }
 
 template <int SRC, bool PAIR, int W, int LDSB>
 __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
@@ -58,25 +56,9 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
     const int k0 = wave * p.run, cols = max(0, min(K - k0, p.run));
     const int steps = (cols + 63) >> 6; // of 64 columns
     const int lastc = ((K + 15) >> 4) - 1; // last chunk of 16 codes of a row
-    const int pitch = p.piece + 16;
+    const int pitch = p.run + 16;
     uint8_t *mine = codes + (FLOATS ? wave * B * pitch : 0);
 
-    // what quantising row b takes is in lane b
-    I8Row row(0);
-    // columns c0 .. c0 + piece - 1 of this wave's run
-    auto quantise = [&](int c0) {
-        const int sh = 31 - __clz(p.piece) - 3, n = min(p.piece, 64 * steps - c0) >> 3; // blocks of 8
-        for (int i0 = 0; i0 < B << sh; i0 += 64) {
-            const int i = i0 + lane, b = min(i >> sh, B - 1), c = i & ((1 << sh) - 1), k = c0 + 8 * c;
-            // (all lanes: a lane's values are read by the others)
-            const I8Row rb(__shfl(row.top, b, 64), __shfl(row.s, b, 64), __shfl(row.r, b, 64));
-            if (i < B << sh && c < n) {
-                I8Load8<FLOATS ? SRC : kF32> v;
-                v.load(p.x, (int64_t)b * K + k0 + k, max(min(cols - k, 8), 0));
-                *reinterpret_cast<uint2 *>(mine + b * pitch + 8 * c) = i8_codes8(v, rb);
-            }
-        }
-    };
     if constexpr (FLOATS) {
         for (int b = 0; b < B; ++b) {
             uint32_t m = 0;
@@ -97,13 +79,20 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 #pragma unroll
             for (int i = 0; i < W; ++i)
                 m = max(m, part[lane][i]);
-        row = I8Row(m);
+        const I8Row row(m); // lane b: row b
         if (wave == 0 && lane < B)
             xscale[lane] = row.s;
+        const int nb = 8 * steps; // blocks of 8 columns of a row
+        for (int b = 0; b < B; ++b) {
+            const I8Row rb(__shfl(row.top, b, 64), __shfl(row.s, b, 64), __shfl(row.r, b, 64));
+            for (int c = lane; c < nb; c += 64) {
+                I8Load8<SRC> v;
+                v.load(p.x, (int64_t)b * K + k0 + 8 * c, max(min(cols - 8 * c, 8), 0));
+                *reinterpret_cast<uint2 *>(mine + b * pitch + 8 * c) = i8_codes8(v, rb);
+            }
+        }
+        lds_wave_order();
     }
-    const bool once = p.piece >= p.run;
-    if (FLOATS && once)
-        quantise(0);
 
     const int tiles = (M + 15) >> 4;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -117,11 +106,6 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
         for (int i = 0; i < P; ++i)
             acc[i] = int4v{0, 0, 0, 0};
         for (int s0 = 0; s0 < steps; s0 += U) {
-            if (FLOATS && !once && (64 * s0) % p.piece == 0) {
-                lds_wave_order();
-                quantise(64 * s0);
-            }
-            lds_wave_order();
             uint4 a[P][U], xv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -137,8 +121,7 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
                 if (s0 + u >= steps)
                     break;
                 if constexpr (FLOATS) {
-                    const int c = (64 * (s0 + u)) & (p.piece - 1);
-                    xv[u] = ld16(mine + xr * pitch + c + 16 * q);
+                    xv[u] = ld16(mine + xr * pitch + 64 * (s0 + u) + 16 * q);
                 } else {
                     const int left = K - (k0 + 64 * (s0 + u) + 16 * q); // codes past K are zero
                     if (__builtin_expect(left < 16, 0)) {
@@ -182,32 +165,31 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
     }
 }
 
-template <int SRC, bool PAIR>
-hipError_t launch_stream(I8StreamArgs p, hipStream_t st)
+// Sixteen waves where K is long enough to keep eight waiting for their weights.
+constexpr int64_t kLongK = 8192;
+// Values a workgroup quantises itself.
+constexpr int64_t kFused = 16384;
+
+template <int SRC, bool PAIR, int W>
+hipError_t launch_waves(I8StreamArgs p, int64_t grid, hipStream_t st)
 {
-    constexpr int W = 8;
-    // LDS for codes: of one row of K up to 16384, or of pieces of 16 rows, which are no shorter
-    // than the columns loaded at once
-    constexpr int kSmall = codes_bytes(W, 1, 2048), kLarge = codes_bytes(W, 16, 512);
-    const int64_t tiles = ((int64_t)p.M + 15) / 16;
+    // a run is at most K / W + 64 columns, and where K is long one row is quantised at most
+    constexpr int B = W == 8 ? 16 : 1;
+    constexpr int LDSB = SRC == kCodes ? 16 : (int)(kFused + W * B * (64 + 16));
+    static_assert(W == 8 || 2 * kLongK >= kFused, "one row");
     p.run = ((p.K + W - 1) / W + 63) / 64 * 64;
-    p.piece = 64;
-    if constexpr (SRC == kCodes) {
-        hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, 16>), dim3((unsigned)tiles), dim3(64 * W), 0,
-                           st, p);
-    } else {
-        while (p.piece < p.run && codes_bytes(W, p.B, 2 * p.piece) <= kLarge)
-            p.piece *= 2;
-        const bool once = p.piece >= p.run;
-        const int64_t grid = once && p.B > 2 ? std::min(tiles, (int64_t)2 * device_cus()) : tiles;
-        if (codes_bytes(W, p.B, p.piece) <= kSmall)
-            hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, kSmall>), dim3((unsigned)grid),
-                               dim3(64 * W), 0, st, p);
-        else
-            hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, kLarge>), dim3((unsigned)grid),
-                               dim3(64 * W), 0, st, p);
-    }
+    if (SRC != kCodes && codes_bytes(W, p.B, p.run) > LDSB)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, LDSB>), dim3((unsigned)grid), dim3(64 * W), 0, st,
+                       p);
     return hipGetLastError();
+}
+
+template <int SRC, bool PAIR>
+hipError_t launch_stream(const I8StreamArgs &p, hipStream_t st)
+{
+    const int64_t tiles = ((int64_t)p.M + 15) / 16;
+    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, tiles, st) : launch_waves<SRC, PAIR, 8>(p, tiles, st);
 }
 
 template <bool PAIR>
@@ -233,6 +215,8 @@ I8StreamArgs args(I8Mat w, I8Mat w2, void *y, int type, int act, int64_t M, int6
 }
 
 } // namespace
+
+bool i8_fused(int64_t K, int64_t B) { return B <= 16 && B * K <= kFused; }
 
 hipError_t launch_gemv_i8(I8Mat w, const void *x, void *y, int type, int64_t M, int64_t K, int B,
                           hipStream_t st)
@@ -277,17 +261,18 @@ hipError_t launch_ffn_i8(const I8FfnArgs &a, hipStream_t st)
     void *h = a.ws + a.off[2];
     const int64_t ldx = (a.H + 15) / 16 * 16, ldh = (a.I + 15) / 16 * 16;
     hipError_t e;
-    if (a.T <= 4) { // two launches
+    if (i8_fused(a.H, a.T)) {
         e = launch_gated_gemv_i8(a.gate, a.up, a.x, h, a.type, a.act, a.I, a.H, (int)a.T, st);
+    } else {
+        e = launch_quantize_i8(a.x, a.type, a.H, xq, ldx, xs, a.T, a.H, st);
         if (e == hipSuccess)
-            e = launch_gemv_i8(a.down, h, a.out, a.type, a.H, a.I, (int)a.T, st);
-        return e;
+            e = launch_gated_i8(a.gate, a.up, {xq, ldx, xs}, h, a.type, a.act, a.I, a.H, a.T, st);
     }
-    e = launch_quantize_i8(a.x, a.type, a.H, xq, ldx, xs, a.T, a.H, st);
-    if (e == hipSuccess)
-        e = launch_gated_i8(a.gate, a.up, {xq, ldx, xs}, h, a.type, a.act, a.I, a.H, a.T, st);
-    if (e == hipSuccess)
-        e = launch_quantize_i8(h, a.type, a.I, hq, ldh, hs, a.T, a.I, st);
+    if (e != hipSuccess)
+        return e;
+    if (i8_fused(a.I, a.T))
+        return launch_gemv_i8(a.down, h, a.out, a.type, a.H, a.I, (int)a.T, st);
+    e = launch_quantize_i8(h, a.type, a.I, hq, ldh, hs, a.T, a.I, st);
     if (e == hipSuccess)
         e = launch_gemm_i8(a.down, {hq, ldh, hs}, a.out, a.type, a.H, a.I, a.T, st);
     return e;

@@ -40,6 +40,7 @@ EXPORTS = (
     "gq_dequant_q4k", "gq_quantize_mxfp4", "gq_dequant_mxfp4", "gq_gemv_mxfp4", "gq_gemm_mxfp4",
     "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes",
     "gq_moe_mxfp4_workspace_offsets", "gq_quantize_i8", "gq_dequant_i8", "gq_gemv_i8",
+    "gq_gemv_i8_workspace_bytes",
     "gq_gemm_i8", "gq_gemm_i8_backward", "gq_gated_i8", "gq_gated_i8_backward",
     "gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8", "gq_ffn_i8_workspace_bytes",
     "gq_last_error", "gq_status_str", "gq_version",
@@ -144,7 +145,7 @@ def lib() -> ctypes.CDLL:
         L.gq_moe_mxfp4_workspace_offsets.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
         for name, args in (("gq_quantize_i8", [vp, ci, i64, vp, i64, vp, i64, i64, vp]),
                            ("gq_dequant_i8", [vp, i64, vp, vp, ci, i64, i64, vp]),
-                           ("gq_gemv_i8", [vp, i64, vp, vp, vp, ci, i64, i64, i64, vp]),
+                           ("gq_gemv_i8", [vp, i64, vp, vp, vp, ci, i64, i64, i64, vp, sz, vp]),
                            ("gq_gemm_i8", [vp, i64, vp] * 2 + [vp, ci, i64, i64, i64, vp]),
                            ("gq_gemm_i8_backward",
                             [vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, vp]),
@@ -160,6 +161,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = sz
             f.argtypes = [i64, i64, i64]
+        L.gq_gemv_i8_workspace_bytes.restype = sz
+        L.gq_gemv_i8_workspace_bytes.argtypes = [i64, i64]
         L.gq_last_error.restype = ctypes.c_char_p
         L.gq_last_error.argtypes = []
         L.gq_status_str.restype = ctypes.c_char_p
@@ -445,9 +448,15 @@ def gq_dequant_i8(q, ldq, s, out, out_type, M, K, stream=None):
     _check(lib().gq_dequant_i8(_at(q), ldq, _ptr(s), _ptr(out), out_type, M, K, _stream(stream)))
 
 
-def gq_gemv_i8(wq, ldw, ws, x, y, dtype, M, K, B, stream=None):
-    _check(lib().gq_gemv_i8(_at(wq), ldw, _ptr(ws), _ptr(x), _ptr(y), dtype, M, K, B,
-                            _stream(stream)))
+def gq_gemv_i8_workspace_bytes(K, B) -> int:
+    return int(lib().gq_gemv_i8_workspace_bytes(K, B))
+
+
+def gq_gemv_i8(wq, ldw, ws, x, y, dtype, M, K, B, wsp=None, ws_bytes=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if wsp is None else wsp.numel() * wsp.element_size()
+    _check(lib().gq_gemv_i8(_at(wq), ldw, _ptr(ws), _ptr(x), _ptr(y), dtype, M, K, B, _ptr(wsp),
+                            ws_bytes, _stream(stream)))
 
 
 def gq_gemm_i8(wq, ldw, ws, xq, ldx, xs, y, y_type, M, K, N, stream=None):
@@ -891,18 +900,24 @@ def dequant_i8(q, s, dtype=None, out=None, stream=None):
     return out
 
 
-def gemv_i8(wq, ws, x, out=None, stream=None):
+def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     """y [B][M] = x [B][K] * W^T in x's dtype (float32, float16 or bfloat16) for int8 W [M][K],
-    1 <= B <= 16, x quantised per row on the way."""
-    _, dev = _mx_enter("x", x)
+    1 <= B <= 16, x quantised per row on the way (from 16384 values on in a workspace, wsp or a
+    new one)."""
+    torch, dev = _mx_enter("x", x)
     qa, ld, sa, M, K = _i8_matrix("W", wq, ws, dev)
     code = _mx_dtype(x.dtype)
     x = _mx_rows("x", x, K)
     xa = _mx_addr("x", x, dev, x.dtype)
     B = x.shape[0]
     y = _mx_new((B, M), x.dtype, x, stream) if out is None else out
+    need = lib().gq_gemv_i8_workspace_bytes(K, B)
+    if need and wsp is None:
+        wsp = _mx_new((need,), torch.uint8, x, stream)
+    wa, wn = (0, 0) if wsp is None else (_mx_addr("wsp", wsp, dev, wsp.dtype),
+                                         wsp.numel() * wsp.element_size())
     _check(lib().gq_gemv_i8(qa, ld, sa, xa, _mx_addr("out", y, dev, x.dtype, (B, M)), code, M, K, B,
-                            _mx_stream(stream, dev)))
+                            wa, wn, _mx_stream(stream, dev)))
     return y
 
 

@@ -61,8 +61,8 @@ def test_dequant_refusals(L):
 def test_gemv_refusals(L):
     f = L.gq_gemv_i8
 
-    def call(wq=P, ldw=64, ws=P, x=P, y=P, t=F32, M=8, K=64, B=1):
-        return f(wq, ldw, ws, x, y, t, M, K, B, None)
+    def call(wq=P, ldw=64, ws=P, x=P, y=P, t=F32, M=8, K=64, B=1, wsp=None, n=0):
+        return f(wq, ldw, ws, x, y, t, M, K, B, wsp, n, None)
 
     for B in (-1, 17):
         refused(L, call(B=B), "GQ_EINVAL", "B = %d" % B)
@@ -76,6 +76,15 @@ def test_gemv_refusals(L):
     refused(L, call(ldw=(1 << 22) + 16), "GQ_ESHAPE", "ldw")
     refused(L, call(ws=BAD), "GQ_EALIGN", "ws")
     refused(L, call(x=None), "GQ_EINVAL", "x is NULL")
+    from quantized_unpack_q4_amd import gq
+    assert gq.gq_gemv_i8_workspace_bytes(1024, 16) == 0
+    need = gq.gq_gemv_i8_workspace_bytes(1025, 16)
+    assert need >= 16 * (1040 + 4)
+    refused(L, call(K=1025, ldw=1040, B=16), "GQ_EWORKSPACE", str(need))
+    refused(L, call(K=1025, ldw=1040, B=16, wsp=P, n=need - 1), "GQ_EWORKSPACE", str(need))
+    refused(L, call(K=1025, ldw=1040, B=16, wsp=BAD, n=need), "GQ_EALIGN", "ws")
+    for args, why in (((0, 1), "K = 0"), ((131072, 1), "K = 131072"), ((64, 17), "B = 17"), ((64, -1), "B = -1")):
+        assert gq.gq_gemv_i8_workspace_bytes(*args) == 0 and why in gq.last_error()
     assert call(M=0, wq=None, ws=None, x=None, y=None) == 0
     assert call(B=0, wq=None, ws=None, x=None, y=None) == 0
 
