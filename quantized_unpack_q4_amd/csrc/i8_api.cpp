@@ -126,6 +126,22 @@ gq_status ffn_shape(const char *fn, int64_t T, int64_t H, int64_t I, size_t off[
     return GQ_OK;
 }
 
+// Gradients of the product: the sizes taken, and the workspace for rows that do not all start
+// 16-byte aligned and hold a multiple of 8 values.
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+gq_status gemm_backward_shape(const char *fn, int64_t M, int64_t N, int64_t ldd, size_t *bytes)
+{
+    GQ_TRY(check_size(fn, "M", M, kMaxGradRows, false));
+    GQ_TRY(check_size(fn, "N", N, kMaxTokens, true));
+    if (N > 1 && ldd < M)
+        return fail(GQ_ESHAPE, "%s: ldd = %lld is below M = %lld", fn, (long long)ldd,
+                    (long long)M);
+    if (N > 1)
+        GQ_TRY(check_most(fn, "ldd", ldd, kMaxGradRows));
+    *bytes = M % 8 != 0 || (N > 1 && ldd % 8 != 0) ? (size_t)N * up8(M) * 2 : 0;
+    return GQ_OK;
+}
+
 // Elements between rows of the gradients of g and u, and the workspace that holds them.
 int64_t grad_ld(int64_t I) { return (I + 63) / 64 * 64; }
 gq_status gated_backward_shape(const char *fn, int64_t N, int64_t H, int64_t I, size_t *bytes)
@@ -263,28 +279,39 @@ gq_status gq_gemm_i8(const int8_t *wq, int64_t ldw, const float *ws, const int8_
 
 gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, const uint16_t *dy,
                               int64_t ldd, uint16_t *dx, int type, int64_t M, int64_t K, int64_t N,
-                              void *stream)
+                              void *wsp, size_t ws_bytes, void *stream)
 {
     static const char fn[] = "gq_gemm_i8_backward";
+    size_t need;
     GQ_TRY(check_type(fn, "type", type, false));
-    GQ_TRY(check_size(fn, "M", M, kMaxGradRows, false));
     GQ_TRY(check_size(fn, "K", K, kMaxK, false));
-    GQ_TRY(check_size(fn, "N", N, kMaxTokens, true));
+    GQ_TRY(gemm_backward_shape(fn, M, N, ldd, &need));
     GQ_TRY(check_most(fn, "the number of outputs", N * K, kMaxOutputs));
     GQ_TRY(check_ld(fn, "ldw", ldw, K, kMaxLd));
     if (N == 0)
         return GQ_OK;
-    if (N > 1 && ldd < M)
-        return fail(GQ_ESHAPE, "%s: ldd = %lld is below M = %lld", fn, (long long)ldd,
-                    (long long)M);
-    if (N > 1)
-        GQ_TRY(check_most(fn, "ldd", ldd, kMaxGradRows));
     GQ_TRY(check_matrix(fn, "wq", wq, "ws", ws));
     GQ_TRY(check_ptr(fn, "dy", dy));
     GQ_TRY(check_ptr(fn, "dx", dx));
+    if (N == 1)
+        ldd = up8(M);
+    if (need) {
+        GQ_TRY(check_ws(fn, "wsp", wsp, ws_bytes, need));
+        GQ_TRY(launched(fn, gq::launch_align_rows(dy, ldd, (uint16_t *)wsp, up8(M), M, N,
+                                                  (hipStream_t)stream)));
+        dy = (const uint16_t *)wsp;
+        ldd = up8(M);
+    }
     const gq::I8GradPart part{{wq, ldw, ws}, dy};
-    return launched(fn, gq::launch_grad_i8(&part, 1, false, N > 1 ? ldd : M, dx, type, M, K, N,
+    return launched(fn, gq::launch_grad_i8(&part, 1, false, ldd, dx, type, M, K, N,
                                            (hipStream_t)stream));
+}
+
+size_t gq_gemm_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t ldd)
+{
+    size_t bytes = 0;
+    return quietly([&] { return gemm_backward_shape("gq_gemm_i8_backward_workspace_bytes", M, N, ldd, &bytes); },
+                   &bytes);
 }
 
 gq_status gq_gated_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,

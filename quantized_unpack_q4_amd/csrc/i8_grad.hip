@@ -1,42 +1,361 @@
-// i8_grad.hip -- gradients through int8 matrices, one output a thread.
+// i8_grad.hip -- gradients through int8 matrices: dx[n][k] = sum_m d[n][m] w16[m][k], 16-bit
+// gradients, weights converted to their type on the way.
+//
+// The sum runs over the weights' rows, so an operand of the matrix product is a column piece.
+// A workgroup of WM x WN waves owns 128 WM columns of the weights by 32 FN WN rows of d, and
+// takes 64 weight rows a stage.  A thread loads a dword (four columns) of eight consecutive
+// rows, straight to registers, forms q s of each column in binary32, rounds and packs the eight
+// rows' values of a column, 16 bytes, and stores them as one chunk of that column's LDS row: the
+// transposition costs nothing, each weight is converted once a workgroup, and both operands of
+// the 32x32x16 products are then read as 16-byte chunks of 128-byte LDS rows.  d goes global ->
+// LDS by direct copies.
+//
+// Column 4 l + i of the tile lies in LDS row (32 WM) i + l: the chunks that a wave stores at a
+// time go to consecutive rows (distinct banks), and a wave's four fragments, i = 0 .. 3 of the
+// same l, hold 128 consecutive columns, sixteen of them consecutive in a lane's accumulators,
+// which are stored as they lie.
+#include <algorithm>
+#include <type_traits>
+
+#include "gq_internal.h"
+#include "gq_lds_dma.h"
 #include "i8_device.h"
+#include "mxfp4_tile.h"
 
 namespace gq {
 
 namespace {
 
-__global__ __launch_bounds__(256) void grad_i8_kernel(I8GradPart p0, I8GradPart p1, int nparts, bool split,
-                                                      int64_t ldd, uint16_t *dx, int type, int M,
-                                                      int K, int64_t total)
+struct GradArgs {
+    I8GradPart part[2];
+    uint16_t *dx;
+    int64_t ldd;
+    int nparts, split;
+    int M, K, N; // d has zeros from M to the next multiple of 8
+    int tiles_k, tiles_total;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float16_t mfma32_16(uint4 a, uint4 b, float16_t c)
 {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= total)
-        return;
-    const int64_t n = t / K, k = t - n * K;
-    float s = 0;
-    for (int p = 0; p < nparts; ++p) {
-        const I8GradPart &a = p ? p1 : p0;
-        for (int m = 0; m < M; ++m) {
-            const float sc = split ? scale_split(a.w.s[m]).pow2 : a.w.s[m];
-            const float wv = as_is((float)a.w.q[m * a.w.ld + k] * sc);
-            const uint32_t r = type == kBF16 ? mx_pack2<true>(wv, 0.f) : mx_pack2<false>(wv, 0.f);
-            const float w16 = type == kBF16 ? __builtin_bit_cast(float, r << 16) : half_to_float(r);
-            s += w16 * (type == kBF16 ? i8_load<kBF16>(a.d, n * ldd + m) : i8_load<kF16>(a.d, n * ldd + m));
-        }
-    }
-    i8_store(dx, t, type, s);
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, a),
+                                                       __builtin_bit_cast(bf8v, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                      __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
 }
 
-unsigned blocks(int64_t total) { return (unsigned)((total + 255) / 256); }
+// Weights of byte `c` of eight rows' dwords (biased by 128) as packed 16-bit values.  The
+// exact q s, rounded to binary32 and then to the type: (q + 128) s - 128 s is exact but for the
+// one rounding of the fused step.
+template <bool BF16, int c>
+__device__ __forceinline__ uint4 weights8(const uint32_t (&w)[8], const float (&s)[8],
+                                          const float (&s128)[8])
+{
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = as_is(fmaf(ubyte_to_float<c>(w[i]), s[i], s128[i]));
+    return make_uint4(mx_pack2<BF16>(v[0], v[1]), mx_pack2<BF16>(v[2], v[3]),
+                      mx_pack2<BF16>(v[4], v[5]), mx_pack2<BF16>(v[6], v[7]));
+}
+
+template <bool BF16, int WM, int WN, int FN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
+{
+    constexpr int NW = WM * WN, NT = 64 * NW, BK = 128 * WM, BN = 32 * FN * WN;
+    constexpr int UN = 8 * (BK / 4) / NT; // 8-row, 4-column units of a thread and stage
+    constexpr int CX = BN / 8 / NW;       // 1 KB copies of d per wave and stage
+    constexpr int kD = 2 * BK * 128;      // byte offset of d in LDS
+    static_assert(UN * NT == 8 * (BK / 4) && CX * 8 * NW == BN, "whole units and copies");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (BK + BN) * 128];
+    const TileWork work = tile_work(p.tiles_total, p.tiles_total);
+    if (work.tile < 0)
+        return;
+    int tk, tn;
+    tile_pos(work.tile, p.tiles_k, p.tiles_total / p.tiles_k, tk, tn);
+    const int k0 = tk * BK, n0 = tn * BN;
+    const int M = p.M, K = p.K;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int r = lane & 31, h = lane >> 5;
+    const int nv = min(p.N - n0, BN);
+    const int nch = (M + 7) >> 3, nst = (nch + 7) >> 3; // chunks of 8 weight rows, stages of a part
+    const int total = p.nparts * nst;
+
+    // d: copy i of this wave: rows 8 (CX wave + i) + lane / 8, slot lane % 8
+    uint32_t doff[CX], dchk[CX];
+#pragma unroll
+    for (int i = 0; i < CX; ++i) {
+        const int row = 8 * (CX * wave + i) + (lane >> 3);
+        doff[i] = (uint32_t)min(row, nv - 1) * (uint32_t)p.ldd * 2u;
+        dchk[i] = (lane & 7) ^ swz8(row);
+    }
+    const uint32_t base = lds_addr(lds);
+    // stage t of the whole sum: stage st of part pt (past the last: the last again)
+    auto where = [&](int t, int &pt, int &st) {
+        t = min(t, total - 1);
+        pt = t >= nst ? 1 : 0;
+        st = t - pt * nst;
+    };
+    auto copy_d = [&](int t, int i) {
+        int pt, st;
+        where(t, pt, st);
+        const uint16_t *d = pt ? p.part[1].d : p.part[0].d;
+        const uint32_t last = (uint32_t)(nch - 1 - 8 * st); // chunks past it repeat it
+        load_lds16(d + (int64_t)n0 * p.ldd + (int64_t)st * 64, doff[i] + 16u * min(dchk[i], last),
+                   __builtin_amdgcn_readfirstlane(base + kD + (t & 1) * (BN * 128) +
+                                                  1024u * (CX * wave + i)));
+    };
+    // weights: unit u of this thread
+    struct Raw {
+        uint32_t w[8];
+        float4 s0, s1;
+    };
+    const int lastcol = ((K + 15) & ~15) - 4;
+    auto load_w = [&](int t, Raw (&raw)[UN]) {
+        int pt, st;
+        where(t, pt, st);
+        const int8_t *q = (pt ? p.part[1].w.q : p.part[0].w.q);
+        const float *s = (pt ? p.part[1].w.s : p.part[0].w.s) + 64 * (int64_t)st;
+        const int64_t ld = pt ? p.part[1].w.ld : p.part[0].w.ld;
+        q += 64 * (int64_t)st * ld;
+        const int left = M - 64 * st; // rows past it repeat the last
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int id = tid + NT * u, m = 8 * (id / (BK / 4)), l = id % (BK / 4);
+            const uint32_t col = (uint32_t)min(k0 + 4 * l, lastcol);
+            if (left >= 64) {
+                const uint32_t off = (uint32_t)m * (uint32_t)ld + col;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    raw[u].w[i] = *reinterpret_cast<const uint32_t *>(q + off + (uint32_t)i * (uint32_t)ld);
+                raw[u].s0 = ldf4(s + m);
+                raw[u].s1 = ldf4(s + m + 4);
+            } else {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int mi = min(m + i, left - 1);
+                    raw[u].w[i] = *reinterpret_cast<const uint32_t *>(q + (uint32_t)mi * (uint32_t)ld + col);
+                    v[i] = s[mi];
+                }
+                raw[u].s0 = make_float4(v[0], v[1], v[2], v[3]);
+                raw[u].s1 = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    };
+    // column i of the units: 16 bytes each into buffer b
+    auto put_w = [&](const Raw (&raw)[UN], auto ic, int b) {
+        constexpr int i = decltype(ic)::value;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int id = tid + NT * u, chunk = id / (BK / 4), row = (BK / 4) * i + id % (BK / 4);
+            uint32_t w[8];
+            float s[8] = {raw[u].s0.x, raw[u].s0.y, raw[u].s0.z, raw[u].s0.w,
+                          raw[u].s1.x, raw[u].s1.y, raw[u].s1.z, raw[u].s1.w};
+            float s128[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                w[j] = raw[u].w[j] ^ 0x80808080u;
+                if (p.split)
+                    s[j] = scale_split(s[j]).pow2;
+                s128[j] = -128.0f * s[j];
+            }
+            *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + row * 128 + 16 * (chunk ^ swz8(row))) =
+                weights8<BF16, i>(w, s, s128);
+        }
+    };
+
+    float16_t acc[4][FN];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = float16_t{};
+    struct Frag {
+        uint4 a[4], b[FN];
+    };
+    uint32_t rof[4]; // (the swizzle of row 32 i + r is that of r)
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        rof[s] = r * 128 + 16 * ((2 * s + h) ^ swz8(r));
+    auto read = [&](int t, int s, Frag &f) {
+        const uint8_t *W = lds + (t & 1) * (BK * 128) + 32 * wm * 128 + rof[s];
+        const uint8_t *D = lds + kD + (t & 1) * (BN * 128) + 32 * FN * wn * 128 + rof[s];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.a[i] = ld16(W + (BK / 4) * i * 128);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            f.b[j] = ld16(D + 32 * j * 128);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](int t, int s, Frag &f) {
+        const int st = t >= nst ? t - nst : t;
+        if (st == nst - 1) { // gradients past M are zero (they may be anything)
+            const bool none = 8 * st + 2 * s + h >= nch;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                f.b[j].x = none ? 0 : f.b[j].x;
+                f.b[j].y = none ? 0 : f.b[j].y;
+                f.b[j].z = none ? 0 : f.b[j].z;
+                f.b[j].w = none ? 0 : f.b[j].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                acc[i][j] = mfma32_16<BF16>(f.a[i], f.b[j], acc[i][j]);
+                asm volatile("" : "+v"(acc[i][j]));
+            }
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+
+    // Stage t: the products of its buffers; its waves put the weights of stage t + 1, loaded
+    // a stage ago, into the other buffers, and start the loads of stage t + 2 and the copies of
+    // d of stage t + 1.  (The compiler does not know that `put` has landed: its wait for that
+    // comes before anything else is in flight.)
+    Frag f0, f1;
+    auto stage = [&](int t, const Raw (&put)[UN], Raw (&load)[UN]) {
+        read(t, 1, f1);
+        put_w(put, I0{}, (t + 1) & 1);
+#pragma unroll
+        for (int i = 0; i < CX; ++i)
+            copy_d(t + 1, i);
+        load_w(t + 2, load);
+        multiply(t, 0, f0);
+        read(t, 2, f0);
+        put_w(put, I1{}, (t + 1) & 1);
+        multiply(t, 1, f1);
+        read(t, 3, f1);
+        put_w(put, I2{}, (t + 1) & 1);
+        multiply(t, 2, f0);
+        put_w(put, I3{}, (t + 1) & 1);
+        multiply(t, 3, f1);
+        // the next stage is converted and copied, and every wave has read this one
+        wait_copies<0>();
+        read(t + 1, 0, f0); // (after the last stage: read and not used)
+    };
+    Raw r0[UN], r1[UN];
+    load_w(0, r0);
+    put_w(r0, I0{}, 0);
+    put_w(r0, I1{}, 0);
+    put_w(r0, I2{}, 0);
+    put_w(r0, I3{}, 0);
+    load_w(1, r1);
+#pragma unroll
+    for (int i = 0; i < CX; ++i)
+        copy_d(0, i);
+    wait_copies<0>();
+    read(0, 0, f0);
+    for (int t = 0; t < total; t += 2) {
+        stage(t, r1, r0);
+        if (t + 1 < total)
+            stage(t + 1, r0, r1);
+    }
+    wait_copies<0>();
+
+    // element v of accumulator i: column 4 (8 (v / 4) + 4 h + v % 4) + i, row r
+    const bool vec = K % 8 == 0; // rows start 16-byte aligned
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int n = 32 * (FN * wn + j) + r;
+        if (n >= nv)
+            break;
+        uint16_t *out = p.dx + (int64_t)(n0 + n) * K;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int k = k0 + 128 * wm + 32 * g + 16 * h;
+            uint32_t o[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                o[2 * c] = mx_pack2<BF16>(acc[0][j][4 * g + c], acc[1][j][4 * g + c]);
+                o[2 * c + 1] = mx_pack2<BF16>(acc[2][j][4 * g + c], acc[3][j][4 * g + c]);
+            }
+            if (vec && k + 16 <= K) {
+                *reinterpret_cast<uint4 *>(out + k) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(out + k + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (k + c < K)
+                        out[k + c] = (uint16_t)(o[c >> 1] >> (16 * (c & 1)));
+            }
+        }
+    }
+}
+
+// Rows of d with M elements of any alignment into rows of ldo (a multiple of 8), zeros behind
+// them.
+__global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *__restrict__ d, int64_t ldd,
+                                                         uint16_t *__restrict__ out, int ldo, int M,
+                                                         int64_t total)
+{
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += step) {
+        const int64_t n = t / (ldo / 8);
+        const int m = (int)(t - n * (ldo / 8)) * 8;
+        I8Load8<kF16> v;
+        v.load(d, n * ldd + m, max(min(M - m, 8), 0));
+        *reinterpret_cast<uint4 *>(out + n * ldo + m) = v.u;
+    }
+}
+
+template <int WM, int WN, int FN>
+hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
+{
+    constexpr int BK = 128 * WM, BN = 32 * FN * WN;
+    p.tiles_k = (p.K + BK - 1) / BK;
+    p.tiles_total = p.tiles_k * ((p.N + BN - 1) / BN);
+    const dim3 grid(tile_grid(p.tiles_total, p.tiles_total)), block(64 * WM * WN);
+    if (type == kBF16)
+        hipLaunchKernelGGL((grad_tile_kernel<true, WM, WN, FN>), grid, block, 0, st, p);
+    else
+        hipLaunchKernelGGL((grad_tile_kernel<false, WM, WN, FN>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+int grad_choice(int64_t K, int64_t N)
+{
+    return N <= 64 ? 64 : (K + 255) / 256 * ((N + 255) / 256) < device_cus() ? 128 : 256;
+}
 
 } // namespace
+
+hipError_t launch_align_rows(const uint16_t *d, int64_t ldd, uint16_t *out, int64_t ldo, int64_t M,
+                             int64_t N, hipStream_t st)
+{
+    const int64_t total = N * (ldo / 8);
+    hipLaunchKernelGGL(align_rows_kernel, dim3((unsigned)std::min((total + 255) / 256, (int64_t)1 << 16)), dim3(256), 0, st, d,
+                       ldd, out, (int)ldo, (int)M, total);
+    return hipGetLastError();
+}
 
 hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
                           uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, hipStream_t st)
 {
-    hipLaunchKernelGGL(grad_i8_kernel, dim3(blocks(K * N)), dim3(256), 0, st, parts[0],
-                       parts[nparts - 1], nparts, split, ldd, dx, type, (int)M, (int)K, K * N);
-    return hipGetLastError();
+    GradArgs p{};
+    p.part[0] = parts[0];
+    p.part[1] = parts[nparts - 1];
+    p.nparts = nparts;
+    p.split = split;
+    p.ldd = ldd;
+    p.dx = dx;
+    p.M = (int)M;
+    p.K = (int)K;
+    p.N = (int)N;
+    switch (grad_choice(K, N)) {
+    case 64: return launch_grad_tiles<1, 2, 1>(p, type, st);
+    case 128: return launch_grad_tiles<1, 4, 1>(p, type, st);
+    default: return launch_grad_tiles<2, 4, 2>(p, type, st);
+    }
 }
 
 } // namespace gq

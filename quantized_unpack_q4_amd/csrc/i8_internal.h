@@ -41,20 +41,26 @@ hipError_t launch_gated_i8(I8Mat gate, I8Mat up, I8Mat x, void *h, int type, int
 hipError_t launch_gated_gemv_i8(I8Mat gate, I8Mat up, const void *x, void *h, int type, int act,
                                 int64_t I, int64_t H, int N, hipStream_t st);
 // The gradients of g and u for a gradient dh [N][I] of h, each times the fraction of its weight
-// row's scale (scale_split): d [N][2][ldd], of dh's 16-bit type.
+// row's scale (scale_split): d [N][2][ldd], of dh's 16-bit type, zeros from I to the next
+// multiple of 8.
 hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *dh, uint16_t *d,
                                  int64_t ldd, int type, int act, int64_t I, int64_t H, int64_t N,
                                  hipStream_t st);
 
 // dx[n][k] = sum over the parts p and rows m < M of d_p[n][m] w16_p[m][k], w16 each weight
-// rounded to the 16-bit type of d and dx; rows of d are ldd elements apart.  split: d holds the
-// fractions of the scales already, weights are codes times their powers of two.
+// rounded to the 16-bit type of d and dx; rows of d are ldd elements apart, a multiple of 8, with
+// zeros from M to the next multiple of 8.  split: d holds the fractions of the scales already,
+// weights are codes times their powers of two.
 struct I8GradPart {
     I8Mat w;
     const uint16_t *d;
 };
 hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
                           uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, hipStream_t st);
+
+// Rows of M 16-bit values, ldd apart, to rows ldo apart (a multiple of 8), zeros behind them.
+hipError_t launch_align_rows(const uint16_t *d, int64_t ldd, uint16_t *out, int64_t ldo, int64_t M,
+                             int64_t N, hipStream_t st);
 
 // The workgroup-tile forms of the products, for more rows than the streaming kernels take.
 hipError_t launch_i8_tiles(I8Mat w, I8Mat x, void *y, int type, int64_t M, int64_t K, int64_t N,

@@ -231,13 +231,15 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
     };
     // weight rows of a store: all of the wave's, or a fragment's where two results are held
     constexpr int G = MODE == kGrads ? 4 : 4 * FW;
+    // (gradients past the last row, up to a multiple of 8, are stored: zeros, as their dh is)
+    const int64_t end = MODE == kGrads ? (M + 7) / 8 * 8 : M;
     auto store = [&](const float4_t(&v)[G], void *y, int64_t n, int left, int64_t m) {
         if (p.type == kF32)
-            store_rows<kF32>(scr, y, n, left, m, M, v, p.ldy);
+            store_rows<kF32>(scr, y, n, left, m, end, v, p.ldy);
         else if (p.type == kF16)
-            store_rows<kF16>(scr, y, n, left, m, M, v, p.ldy);
+            store_rows<kF16>(scr, y, n, left, m, end, v, p.ldy);
         else
-            store_rows<kBF16>(scr, y, n, left, m, M, v, p.ldy);
+            store_rows<kBF16>(scr, y, n, left, m, end, v, p.ldy);
     };
 #pragma unroll
     for (int j = 0; j < FN; ++j) {

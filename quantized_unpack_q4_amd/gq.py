@@ -41,7 +41,7 @@ EXPORTS = (
     "gq_gemm_mxfp4_mxfp4", "gq_moe_gemm_mxfp4", "gq_moe_mxfp4_workspace_bytes",
     "gq_moe_mxfp4_workspace_offsets", "gq_quantize_i8", "gq_dequant_i8", "gq_gemv_i8",
     "gq_gemv_i8_workspace_bytes",
-    "gq_gemm_i8", "gq_gemm_i8_backward", "gq_gated_i8", "gq_gated_i8_backward",
+    "gq_gemm_i8", "gq_gemm_i8_backward", "gq_gemm_i8_backward_workspace_bytes", "gq_gated_i8", "gq_gated_i8_backward",
     "gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8", "gq_ffn_i8_workspace_bytes",
     "gq_last_error", "gq_status_str", "gq_version",
 )
@@ -148,7 +148,7 @@ def lib() -> ctypes.CDLL:
                            ("gq_gemv_i8", [vp, i64, vp, vp, vp, ci, i64, i64, i64, vp, sz, vp]),
                            ("gq_gemm_i8", [vp, i64, vp] * 2 + [vp, ci, i64, i64, i64, vp]),
                            ("gq_gemm_i8_backward",
-                            [vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, vp]),
+                            [vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, vp, sz, vp]),
                            ("gq_gated_i8", [vp, i64, vp] * 3 + [vp, ci, ci, i64, i64, i64, vp]),
                            ("gq_gated_i8_backward",
                             [vp, i64, vp] * 3 + [vp, vp, ci, ci, i64, i64, i64, vp, sz, vp]),
@@ -157,7 +157,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = st
             f.argtypes = args
-        for name in ("gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8_workspace_bytes"):
+        for name in ("gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8_workspace_bytes",
+                     "gq_gemm_i8_backward_workspace_bytes"):
             f = getattr(L, name)
             f.restype = sz
             f.argtypes = [i64, i64, i64]
@@ -464,9 +465,16 @@ def gq_gemm_i8(wq, ldw, ws, xq, ldx, xs, y, y_type, M, K, N, stream=None):
                             N, _stream(stream)))
 
 
-def gq_gemm_i8_backward(wq, ldw, ws, dy, ldd, dx, dtype, M, K, N, stream=None):
+def gq_gemm_i8_backward_workspace_bytes(M, N, ldd) -> int:
+    return int(lib().gq_gemm_i8_backward_workspace_bytes(M, N, ldd))
+
+
+def gq_gemm_i8_backward(wq, ldw, ws, dy, ldd, dx, dtype, M, K, N, wsp=None, ws_bytes=None,
+                        stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if wsp is None else wsp.numel() * wsp.element_size()
     _check(lib().gq_gemm_i8_backward(_at(wq), ldw, _ptr(ws), _at(dy), ldd, _ptr(dx), dtype, M, K,
-                                     N, _stream(stream)))
+                                     N, _ptr(wsp), ws_bytes, _stream(stream)))
 
 
 def gq_gated_i8(wq_gate, ld_gate, ws_gate, wq_up, ld_up, ws_up, xq, ldx, xs, h, h_type, act, I, H,
@@ -867,6 +875,15 @@ def _rows_2d(name, x):
     return rows, K, ld if rows > 1 else K
 
 
+def _i8_wsp(name, wsp, need, like, dev, stream):
+    """(address, bytes) of a workspace that some sizes need, a new one where none is given."""
+    if wsp is None:
+        if not need:
+            return 0, 0
+        wsp = _mx_new((need,), _torch.uint8, like, stream)
+    return _mx_addr(name, wsp, dev, wsp.dtype), wsp.numel() * wsp.element_size()
+
+
 def quantize_i8(x, out=None, stream=None):
     """x [N][K] (float32, float16 or bfloat16; rows contiguous, any distance apart) -> (codes
     int8 [N][K] with rows a multiple of 16 bytes apart, scales float32 [N]); x may be the
@@ -904,7 +921,7 @@ def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     """y [B][M] = x [B][K] * W^T in x's dtype (float32, float16 or bfloat16) for int8 W [M][K],
     1 <= B <= 16, x quantised per row on the way (from 16384 values on in a workspace, wsp or a
     new one)."""
-    torch, dev = _mx_enter("x", x)
+    _, dev = _mx_enter("x", x)
     qa, ld, sa, M, K = _i8_matrix("W", wq, ws, dev)
     code = _mx_dtype(x.dtype)
     x = _mx_rows("x", x, K)
@@ -912,12 +929,8 @@ def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     B = x.shape[0]
     y = _mx_new((B, M), x.dtype, x, stream) if out is None else out
     need = lib().gq_gemv_i8_workspace_bytes(K, B)
-    if need and wsp is None:
-        wsp = _mx_new((need,), torch.uint8, x, stream)
-    wa, wn = (0, 0) if wsp is None else (_mx_addr("wsp", wsp, dev, wsp.dtype),
-                                         wsp.numel() * wsp.element_size())
     _check(lib().gq_gemv_i8(qa, ld, sa, xa, _mx_addr("out", y, dev, x.dtype, (B, M)), code, M, K, B,
-                            wa, wn, _mx_stream(stream, dev)))
+                            *_i8_wsp("wsp", wsp, need, x, dev, stream), _mx_stream(stream, dev)))
     return y
 
 
@@ -938,10 +951,11 @@ def gemm_i8(wq, ws, xq, xs, dtype=None, out=None, stream=None):
     return y
 
 
-def gemm_i8_backward(wq, ws, dy, out=None, stream=None):
+def gemm_i8_backward(wq, ws, dy, wsp=None, out=None, stream=None):
     """dX [N][K] = dY [N][M] * W in dY's dtype (float16 or bfloat16): the gradient of the values
     of X for a gradient dY of gemm_i8's (or gemv_i8's) result; rows of dY contiguous, any
-    distance apart."""
+    distance apart (where they do not all start 16-byte aligned, they are copied into a
+    workspace, wsp or a new one)."""
     _, dev = _mx_enter("dY", dy)
     wa, ldw, wsa, M, K = _i8_matrix("W", wq, ws, dev)
     code = _mx_dtype(dy.dtype, f32=False)
@@ -949,8 +963,10 @@ def gemm_i8_backward(wq, ws, dy, out=None, stream=None):
     if MD != M:
         raise ValueError("dY has rows of %d values, expected %d" % (MD, M))
     dx = _mx_new((N, K), dy.dtype, dy, stream) if out is None else out
+    need = lib().gq_gemm_i8_backward_workspace_bytes(M, N, ldd)
     _check(lib().gq_gemm_i8_backward(wa, ldw, wsa, dy.data_ptr(), ldd,
                                      _mx_addr("out", dx, dev, dy.dtype, (N, K)), code, M, K, N,
+                                     *_i8_wsp("wsp", wsp, need, dy, dev, stream),
                                      _mx_stream(stream, dev)))
     return dx
 

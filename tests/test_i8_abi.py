@@ -112,8 +112,18 @@ def test_gemm_refusals(L):
 def test_gemm_backward_refusals(L):
     f = L.gq_gemm_i8_backward
 
-    def call(wq=P, ldw=64, ws=P, dy=P, ldd=8, dx=P, t=F16, M=8, K=64, N=2):
-        return f(wq, ldw, ws, dy, ldd, dx, t, M, K, N, None)
+    from quantized_unpack_q4_amd import gq
+    size = gq.gq_gemm_i8_backward_workspace_bytes
+    assert size(8, 2, 16) == 0 and size(8, 1, 3) == 0 and size(8, 0, 8) == 0
+    assert size(8, 2, 9) == 2 * 8 * 2 and size(9, 2, 16) == 2 * 16 * 2 and size(9, 1, 0) == 32
+    assert size(8, 2, 7) == 0 and "ldd = 7" in gq.last_error()
+
+    def call(wq=P, ldw=64, ws=P, dy=P, ldd=8, dx=P, t=F16, M=8, K=64, N=2, wsp=None, n=0):
+        return f(wq, ldw, ws, dy, ldd, dx, t, M, K, N, wsp, n, None)
+
+    refused(L, call(ldd=9), "GQ_EWORKSPACE", "wsp", "32")
+    refused(L, call(ldd=9, wsp=P, n=31), "GQ_EWORKSPACE", "32")
+    refused(L, call(ldd=9, wsp=BAD, n=32), "GQ_EALIGN", "wsp")
 
     refused(L, call(t=F32), "GQ_EINVAL", "type = 0")
     refused(L, call(M=0), "GQ_EINVAL", "M = 0")
