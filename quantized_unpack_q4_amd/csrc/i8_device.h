@@ -17,6 +17,23 @@ namespace gq {
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 
+// An address that is the same in all lanes, for scalar registers.
+__device__ __forceinline__ const int8_t *uniform(const int8_t *p)
+{
+    const uint64_t a = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    return (const int8_t *)((uint64_t)hi << 32 | lo);
+}
+
+// The dword at a byte offset from such an address.
+__device__ __forceinline__ uint32_t load_dword(const int8_t *base, uint32_t off)
+{
+    typedef const __attribute__((address_space(1))) int8_t *Global;
+    typedef const __attribute__((address_space(1))) uint32_t *GlobalWord;
+    return *(GlobalWord)((Global)(uint64_t)uniform(base) + off);
+}
+
 // What quantising a row takes: its largest magnitude, the scale (NaN for a row with an
 // infinity or a NaN, whose codes are zero) and the factor of the quotient; r < 0 for rows of
 // very small values, where 127 / max could be infinite: all their codes come from binary64.
@@ -171,20 +188,17 @@ __device__ __forceinline__ float i8_scaled(int sum, float ws, float xs)
     return as_is((float)sum * ws * xs);
 }
 
-// A weight row's scale as f times a power of two, f in [1/2, 1): codes times the power of two
-// are exact in both 16-bit types (in binary16 for scales from 2^-25 to 2^8), so that where f
-// can go into the other operand before its rounding, a product rounds one operand only.
-struct ScaleSplit {
-    float f, pow2;
-};
-__device__ __forceinline__ ScaleSplit scale_split(float s)
+// A weight row's scale as f P, P a power of two and f in [1/2, 1): codes times P are exact in
+// both 16-bit types (in binary16 for scales from 2^-25 to 2^8), so that where f can go into
+// the other operand before its rounding, a product rounds one operand only.  P stays between
+// 2^-126 and 2^127; what that leaves (zero, subnormal and the largest scales, infinity, NaN)
+// is f's.
+__device__ __forceinline__ float scale_pow2(float s)
 {
-    const uint32_t b = __builtin_bit_cast(uint32_t, s), e = b & 0x7f800000u;
-    if (e == 0 || e >= 0x7f000000u) // zero and subnormal; the last binade, infinity, NaN
-        return {1.0f, s};
-    return {__builtin_bit_cast(float, (b & 0x007fffffu) | 0x3f000000u),
-            __builtin_bit_cast(float, (b & 0xff800000u) + 0x00800000u)};
+    const uint32_t e = __builtin_bit_cast(uint32_t, s) & 0x7f800000u;
+    return __builtin_bit_cast(float, min(e + 0x00800000u, 0x7f000000u));
 }
+__device__ __forceinline__ float scale_fraction(float s) { return s * (1.0f / scale_pow2(s)); }
 
 // Four consecutive 16-bit values from element i (any alignment), of which n exist.
 __device__ __forceinline__ float4_t load4(const uint16_t *x, int64_t i, int64_t n, int type)

@@ -30,7 +30,7 @@ struct GradArgs {
     I8GradPart part[2];
     uint16_t *dx;
     int64_t ldd;
-    int nparts, split;
+    int nparts;
     int M, K, N; // d has zeros from M to the next multiple of 8
     int tiles_k, tiles_total;
 };
@@ -46,22 +46,20 @@ __device__ __forceinline__ float16_t mfma32_16(uint4 a, uint4 b, float16_t c)
                                                       __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
 }
 
-// Weights of byte `c` of eight rows' dwords (biased by 128) as packed 16-bit values.  The
-// exact q s, rounded to binary32 and then to the type: (q + 128) s - 128 s is exact but for the
-// one rounding of the fused step.
+// Weights of byte `c` of eight rows' dwords as packed 16-bit values: q s rounded to binary32 and
+// then to the type.
 template <bool BF16, int c>
-__device__ __forceinline__ uint4 weights8(const uint32_t (&w)[8], const float (&s)[8],
-                                          const float (&s128)[8])
+__device__ __forceinline__ uint4 weights8(const uint32_t (&w)[8], const float (&s)[8])
 {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        v[i] = as_is(fmaf(ubyte_to_float<c>(w[i]), s[i], s128[i]));
+        v[i] = as_is((float)(int8_t)(w[i] >> (8 * c)) * s[i]);
     return make_uint4(mx_pack2<BF16>(v[0], v[1]), mx_pack2<BF16>(v[2], v[3]),
                       mx_pack2<BF16>(v[4], v[5]), mx_pack2<BF16>(v[6], v[7]));
 }
 
-template <bool BF16, int WM, int WN, int FN>
+template <bool BF16, bool SPLIT, int WM, int WN, int FN, bool TAIL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
 {
     constexpr int NW = WM * WN, NT = 64 * NW, BK = 128 * WM, BN = 32 * FN * WN;
@@ -105,68 +103,76 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         where(t, pt, st);
         const uint16_t *d = pt ? p.part[1].d : p.part[0].d;
         const uint32_t last = (uint32_t)(nch - 1 - 8 * st); // chunks past it repeat it
-        load_lds16(d + (int64_t)n0 * p.ldd + (int64_t)st * 64, doff[i] + 16u * min(dchk[i], last),
+        load_lds16(d + (int64_t)n0 * p.ldd + (int64_t)st * 64, doff[i] + 16u * (TAIL ? min(dchk[i], last) : dchk[i]),
                    __builtin_amdgcn_readfirstlane(base + kD + (t & 1) * (BN * 128) +
                                                   1024u * (CX * wave + i)));
     };
-    // weights: unit u of this thread
+    // weights: unit u of this thread, rows 8 c .. 8 c + 7 of columns 4 l .. 4 l + 3
     struct Raw {
         uint32_t w[8];
-        float4 s0, s1;
+        float s[8];
     };
     const int lastcol = ((K + 15) & ~15) - 4;
+    int urow[UN], ucol[UN], uput[UN][4];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+        const int id = tid + NT * u, c = id / (BK / 4), l = id % (BK / 4);
+        urow[u] = 8 * c;
+        ucol[u] = min(k0 + 4 * l, lastcol);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (BK / 4) * i + l;
+            uput[u][i] = row * 128 + 16 * (c ^ swz8(row));
+        }
+    }
     auto load_w = [&](int t, Raw (&raw)[UN]) {
         int pt, st;
         where(t, pt, st);
-        const int8_t *q = (pt ? p.part[1].w.q : p.part[0].w.q);
-        const float *s = (pt ? p.part[1].w.s : p.part[0].w.s) + 64 * (int64_t)st;
-        const int64_t ld = pt ? p.part[1].w.ld : p.part[0].w.ld;
+        const int8_t *q = pt ? p.part[1].w.q + 0 : p.part[0].w.q + 0;
+        const float *s = (pt ? p.part[1].w.s + 0 : p.part[0].w.s + 0) + 64 * (int64_t)st;
+        const uint32_t ld = (uint32_t)(pt ? p.part[1].w.ld + 0 : p.part[0].w.ld + 0);
         q += 64 * (int64_t)st * ld;
         const int left = M - 64 * st; // rows past it repeat the last
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            const int id = tid + NT * u, m = 8 * (id / (BK / 4)), l = id % (BK / 4);
-            const uint32_t col = (uint32_t)min(k0 + 4 * l, lastcol);
-            if (left >= 64) {
-                const uint32_t off = (uint32_t)m * (uint32_t)ld + col;
+            if (!TAIL || left >= 64) {
+                const uint32_t off = (uint32_t)urow[u] * ld + (uint32_t)ucol[u];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    raw[u].w[i] = *reinterpret_cast<const uint32_t *>(q + off + (uint32_t)i * (uint32_t)ld);
-                raw[u].s0 = ldf4(s + m);
-                raw[u].s1 = ldf4(s + m + 4);
+                    raw[u].w[i] = load_dword(q + (uint64_t)i * ld, off);
+                *reinterpret_cast<float4 *>(raw[u].s) = ldf4(s + urow[u]);
+                *reinterpret_cast<float4 *>(raw[u].s + 4) = ldf4(s + urow[u] + 4);
             } else {
-                float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int mi = min(m + i, left - 1);
-                    raw[u].w[i] = *reinterpret_cast<const uint32_t *>(q + (uint32_t)mi * (uint32_t)ld + col);
-                    v[i] = s[mi];
+                    const int m = min(urow[u] + i, left - 1);
+                    raw[u].w[i] = load_dword(q, (uint32_t)m * ld + (uint32_t)ucol[u]);
+                    raw[u].s[i] = s[m];
                 }
-                raw[u].s0 = make_float4(v[0], v[1], v[2], v[3]);
-                raw[u].s1 = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
+    };
+    // once loaded: a tile of 256 columns has one unit's rows in all lanes of a wave, their scales
+    // then go to scalar registers
+    auto ready = [&](Raw (&raw)[UN]) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (BK == 256)
+                    raw[u].s[i] = __builtin_bit_cast(
+                        float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, raw[u].s[i])));
+                if constexpr (SPLIT)
+                    raw[u].s[i] = scale_pow2(raw[u].s[i]);
+            }
     };
     // column i of the units: 16 bytes each into buffer b
     auto put_w = [&](const Raw (&raw)[UN], auto ic, int b) {
         constexpr int i = decltype(ic)::value;
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int id = tid + NT * u, chunk = id / (BK / 4), row = (BK / 4) * i + id % (BK / 4);
-            uint32_t w[8];
-            float s[8] = {raw[u].s0.x, raw[u].s0.y, raw[u].s0.z, raw[u].s0.w,
-                          raw[u].s1.x, raw[u].s1.y, raw[u].s1.z, raw[u].s1.w};
-            float s128[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                w[j] = raw[u].w[j] ^ 0x80808080u;
-                if (p.split)
-                    s[j] = scale_split(s[j]).pow2;
-                s128[j] = -128.0f * s[j];
-            }
-            *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + row * 128 + 16 * (chunk ^ swz8(row))) =
-                weights8<BF16, i>(w, s, s128);
-        }
+        for (int u = 0; u < UN; ++u)
+            *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + uput[u][i]) =
+                weights8<BF16, i>(raw[u].w, raw[u].s);
     };
 
     float16_t acc[4][FN];
@@ -194,8 +200,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         __builtin_amdgcn_sched_barrier(0);
     };
     auto multiply = [&](int t, int s, Frag &f) {
-        const int st = t >= nst ? t - nst : t;
-        if (st == nst - 1) { // gradients past M are zero (they may be anything)
+        if constexpr (TAIL) { // gradients past M are zero (they may be anything)
+            const int st = t >= nst ? t - nst : t;
             const bool none = 8 * st + 2 * s + h >= nch;
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
@@ -223,8 +229,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     // d of stage t + 1.  (The compiler does not know that `put` has landed: its wait for that
     // comes before anything else is in flight.)
     Frag f0, f1;
-    auto stage = [&](int t, const Raw (&put)[UN], Raw (&load)[UN]) {
+    auto stage = [&](int t, Raw (&put)[UN], Raw (&load)[UN]) {
         read(t, 1, f1);
+        ready(put);
         put_w(put, I0{}, (t + 1) & 1);
 #pragma unroll
         for (int i = 0; i < CX; ++i)
@@ -245,6 +252,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     };
     Raw r0[UN], r1[UN];
     load_w(0, r0);
+    ready(r0);
     put_w(r0, I0{}, 0);
     put_w(r0, I1{}, 0);
     put_w(r0, I2{}, 0);
@@ -308,23 +316,37 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *__restr
     }
 }
 
-template <int WM, int WN, int FN>
+template <bool SPLIT, int WM, int WN, int FN>
 hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
 {
     constexpr int BK = 128 * WM, BN = 32 * FN * WN;
     p.tiles_k = (p.K + BK - 1) / BK;
     p.tiles_total = p.tiles_k * ((p.N + BN - 1) / BN);
     const dim3 grid(tile_grid(p.tiles_total, p.tiles_total)), block(64 * WM * WN);
+    auto launch = [&](auto bf16, auto tail) {
+        hipLaunchKernelGGL((grad_tile_kernel<decltype(bf16)::value, SPLIT, WM, WN, FN, decltype(tail)::value>),
+                           grid, block, 0, st, p);
+    };
     if (type == kBF16)
-        hipLaunchKernelGGL((grad_tile_kernel<true, WM, WN, FN>), grid, block, 0, st, p);
+        p.M % 64 ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
     else
-        hipLaunchKernelGGL((grad_tile_kernel<false, WM, WN, FN>), grid, block, 0, st, p);
+        p.M % 64 ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
     return hipGetLastError();
 }
 
 int grad_choice(int64_t K, int64_t N)
 {
     return N <= 64 ? 64 : (K + 255) / 256 * ((N + 255) / 256) < device_cus() ? 128 : 256;
+}
+
+template <bool SPLIT>
+hipError_t launch_grad(const GradArgs &p, int type, hipStream_t st)
+{
+    switch (grad_choice(p.K, p.N)) {
+    case 64: return launch_grad_tiles<SPLIT, 1, 2, 1>(p, type, st);
+    case 128: return launch_grad_tiles<SPLIT, 1, 4, 1>(p, type, st);
+    default: return launch_grad_tiles<SPLIT, 2, 4, 2>(p, type, st);
+    }
 }
 
 } // namespace
@@ -345,17 +367,12 @@ hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64
     p.part[0] = parts[0];
     p.part[1] = parts[nparts - 1];
     p.nparts = nparts;
-    p.split = split;
     p.ldd = ldd;
     p.dx = dx;
     p.M = (int)M;
     p.K = (int)K;
     p.N = (int)N;
-    switch (grad_choice(K, N)) {
-    case 64: return launch_grad_tiles<1, 2, 1>(p, type, st);
-    case 128: return launch_grad_tiles<1, 4, 1>(p, type, st);
-    default: return launch_grad_tiles<2, 4, 2>(p, type, st);
-    }
+    return split ? launch_grad<true>(p, type, st) : launch_grad<false>(p, type, st);
 }
 
 } // namespace gq

@@ -41,7 +41,7 @@ hipError_t launch_gated_i8(I8Mat gate, I8Mat up, I8Mat x, void *h, int type, int
 hipError_t launch_gated_gemv_i8(I8Mat gate, I8Mat up, const void *x, void *h, int type, int act,
                                 int64_t I, int64_t H, int N, hipStream_t st);
 // The gradients of g and u for a gradient dh [N][I] of h, each times the fraction of its weight
-// row's scale (scale_split): d [N][2][ldd], of dh's 16-bit type, zeros from I to the next
+// row's scale (scale_fraction): d [N][2][ldd], of dh's 16-bit type, zeros from I to the next
 // multiple of 8.
 hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *dh, uint16_t *d,
                                  int64_t ldd, int type, int act, int64_t I, int64_t H, int64_t N,

@@ -45,15 +45,6 @@ __device__ __forceinline__ int16v mfma_i8(uint4 a, uint4 b, int16v c)
                                                  __builtin_bit_cast(int4v, b), c, 0, 0, 0);
 }
 
-// An address that is the same in all lanes, for scalar registers.
-__device__ __forceinline__ const int8_t *uniform(const int8_t *p)
-{
-    const uint64_t a = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-    return (const int8_t *)((uint64_t)hi << 32 | lo);
-}
-
 template <int WM, int WN, int FM, int FN, int NB>
 constexpr int i8_lds_bytes()
 {
@@ -270,8 +261,8 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const Gate a = gate_grad(g[c], p.act);
-                            dg[c] = d[c] * u[c] * a.da * scale_split(ws[c]).f;
-                            du[c] = d[c] * a.a * scale_split(us[c]).f;
+                            dg[c] = d[c] * u[c] * a.da * scale_fraction(ws[c]);
+                            du[c] = d[c] * a.a * scale_fraction(us[c]);
                         }
                         v[v4] = dg;
                         v2[v4] = du;
