@@ -591,17 +591,19 @@ gq_status gq_gemm_i8(const int8_t *wq, int64_t ldw, const float *ws, const int8_
  *   dX[n][k] = round( sum_m dY[n][m] * w16[m][k] ), sums binary32, one rounding,
  * w16 = ws[m] * wq[m][k] rounded to `type` (GQ_F16 or GQ_BF16; the weights of the other
  * 16-bit products are rounded so, too).  dy: [N] rows of M elements of `type`, ldd >= M
- * elements apart (ldd unused when N is 1).  dx: [N][K] of `type`.  Where M and ldd are
- * multiples of 8 no workspace is taken (wsp may be NULL); otherwise dy's rows are first copied
- * into wsp, at least gq_gemm_i8_backward_workspace_bytes(M, N, ldd) bytes, 16-byte aligned,
- * contents on entry ignored; not to be in use by another call while this one runs.
+ * elements apart (ldd unused when N is 1).  dx: [N][K] of `type`.  wsp: at least
+ * gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd) bytes, 16-byte aligned, contents on entry
+ * ignored; not to be in use by another call while this one runs; it may be NULL where that is
+ * zero.  It holds dy's rows where M and ldd are not both multiples of 8, and, where the result
+ * has too few tiles to fill the device, binary32 sums of runs of the sum over m, which are then
+ * added in run order (results do not vary from call to call).
  * Requires K <= 131071, 1 <= M <= 2^22, ldd <= 2^22, N <= 2^21, N*K <= 2^37, ldw <= 2^22. */
 gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, const uint16_t *dy,
                               int64_t ldd, uint16_t *dx, int type, int64_t M, int64_t K, int64_t N,
                               void *wsp, size_t ws_bytes, void *stream);
 /* Its workspace size: 0 where it needs none (and, with the reason in gq_last_error(), for sizes
  * it does not take). */
-size_t gq_gemm_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t ldd);
+size_t gq_gemm_i8_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t ldd);
 
 /* Activations of the gated feed-forward block: act(z) = z sigmoid(p(z)). */
 typedef enum gq_act {

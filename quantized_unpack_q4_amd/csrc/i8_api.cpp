@@ -126,30 +126,39 @@ gq_status ffn_shape(const char *fn, int64_t T, int64_t H, int64_t I, size_t off[
     return GQ_OK;
 }
 
-// Gradients of the product: the sizes taken, and the workspace for rows that do not all start
-// 16-byte aligned and hold a multiple of 8 values.
+// Gradients of the product: the sizes taken, and the workspace: dy's rows where they do not all
+// start 16-byte aligned and hold a multiple of 8 values, the sums of its runs, total.
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
-gq_status gemm_backward_shape(const char *fn, int64_t M, int64_t N, int64_t ldd, size_t *bytes)
+gq_status gemm_backward_shape(const char *fn, int64_t M, int64_t K, int64_t N, int64_t ldd,
+                              size_t off[3])
 {
     GQ_TRY(check_size(fn, "M", M, kMaxGradRows, false));
+    GQ_TRY(check_size(fn, "K", K, kMaxK, false));
     GQ_TRY(check_size(fn, "N", N, kMaxTokens, true));
+    GQ_TRY(check_most(fn, "the number of outputs", N * K, kMaxOutputs));
     if (N > 1 && ldd < M)
         return fail(GQ_ESHAPE, "%s: ldd = %lld is below M = %lld", fn, (long long)ldd,
                     (long long)M);
     if (N > 1)
         GQ_TRY(check_most(fn, "ldd", ldd, kMaxGradRows));
-    *bytes = M % 8 != 0 || (N > 1 && ldd % 8 != 0) ? (size_t)N * up8(M) * 2 : 0;
+    const bool align = N > 0 && (M % 8 != 0 || (N > 1 && ldd % 8 != 0));
+    off[0] = 0;
+    off[1] = align ? up((size_t)N * up8(M) * 2) : 0;
+    off[2] = N > 0 ? off[1] + gq::grad_partial_bytes(1, M, K, N) : 0;
     return GQ_OK;
 }
 
-// Elements between rows of the gradients of g and u, and the workspace that holds them.
+// The gated half's: the gradients of g and u, rows of each so many elements apart; the sums of
+// the runs; total.
 int64_t grad_ld(int64_t I) { return (I + 63) / 64 * 64; }
-gq_status gated_backward_shape(const char *fn, int64_t N, int64_t H, int64_t I, size_t *bytes)
+gq_status gated_backward_shape(const char *fn, int64_t N, int64_t H, int64_t I, size_t off[3])
 {
     GQ_TRY(product_sizes(fn, "I", I, "H", H, "N", N));
     GQ_TRY(check_most(fn, "I", I, kMaxGradRows / 2));
     GQ_TRY(check_most(fn, "N*H", N * H, kMaxOutputs));
-    *bytes = (size_t)N * 2 * grad_ld(I) * 2;
+    off[0] = 0;
+    off[1] = up((size_t)N * 2 * grad_ld(I) * 2);
+    off[2] = off[1] + (N > 0 && I > 0 ? gq::grad_partial_bytes(2, I, H, N) : 0);
     return GQ_OK;
 }
 
@@ -282,21 +291,20 @@ gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, co
                               void *wsp, size_t ws_bytes, void *stream)
 {
     static const char fn[] = "gq_gemm_i8_backward";
-    size_t need;
+    size_t off[3];
     GQ_TRY(check_type(fn, "type", type, false));
-    GQ_TRY(check_size(fn, "K", K, kMaxK, false));
-    GQ_TRY(gemm_backward_shape(fn, M, N, ldd, &need));
-    GQ_TRY(check_most(fn, "the number of outputs", N * K, kMaxOutputs));
+    GQ_TRY(gemm_backward_shape(fn, M, K, N, ldd, off));
     GQ_TRY(check_ld(fn, "ldw", ldw, K, kMaxLd));
     if (N == 0)
         return GQ_OK;
     GQ_TRY(check_matrix(fn, "wq", wq, "ws", ws));
     GQ_TRY(check_ptr(fn, "dy", dy));
     GQ_TRY(check_ptr(fn, "dx", dx));
+    if (off[2])
+        GQ_TRY(check_ws(fn, "wsp", wsp, ws_bytes, off[2]));
     if (N == 1)
         ldd = up8(M);
-    if (need) {
-        GQ_TRY(check_ws(fn, "wsp", wsp, ws_bytes, need));
+    if (off[1]) {
         GQ_TRY(launched(fn, gq::launch_align_rows(dy, ldd, (uint16_t *)wsp, up8(M), M, N,
                                                   (hipStream_t)stream)));
         dy = (const uint16_t *)wsp;
@@ -304,14 +312,14 @@ gq_status gq_gemm_i8_backward(const int8_t *wq, int64_t ldw, const float *ws, co
     }
     const gq::I8GradPart part{{wq, ldw, ws}, dy};
     return launched(fn, gq::launch_grad_i8(&part, 1, false, ldd, dx, type, M, K, N,
-                                           (hipStream_t)stream));
+                                           (char *)wsp + off[1], (hipStream_t)stream));
 }
 
-size_t gq_gemm_i8_backward_workspace_bytes(int64_t M, int64_t N, int64_t ldd)
+size_t gq_gemm_i8_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t ldd)
 {
-    size_t bytes = 0;
-    return quietly([&] { return gemm_backward_shape("gq_gemm_i8_backward_workspace_bytes", M, N, ldd, &bytes); },
-                   &bytes);
+    size_t off[3] = {};
+    return quietly([&] { return gemm_backward_shape("gq_gemm_i8_backward_workspace_bytes", M, K, N, ldd, off); },
+                   &off[2]);
 }
 
 gq_status gq_gated_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,
@@ -339,9 +347,9 @@ gq_status gq_gated_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_ga
 
 size_t gq_gated_i8_backward_workspace_bytes(int64_t N, int64_t H, int64_t I)
 {
-    size_t bytes = 0;
-    return quietly([&] { return gated_backward_shape("gq_gated_i8_backward_workspace_bytes", N, H, I, &bytes); },
-                   &bytes);
+    size_t off[3] = {};
+    return quietly([&] { return gated_backward_shape("gq_gated_i8_backward_workspace_bytes", N, H, I, off); },
+                   &off[2]);
 }
 
 gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,
@@ -351,10 +359,10 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
                                void *ws, size_t ws_bytes, void *stream)
 {
     static const char fn[] = "gq_gated_i8_backward";
-    size_t need;
+    size_t off[3];
     GQ_TRY(check_type(fn, "type", type, false));
     GQ_TRY(check_act(fn, act));
-    GQ_TRY(gated_backward_shape(fn, N, H, I, &need));
+    GQ_TRY(gated_backward_shape(fn, N, H, I, off));
     if (I == 0)
         return fail(GQ_EINVAL, "%s: I = 0 must be positive", fn);
     GQ_TRY(check_ld(fn, "ld_gate", ld_gate, H, kMaxLd));
@@ -367,7 +375,7 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
     GQ_TRY(check_matrix(fn, "xq", xq, "xs", xs));
     GQ_TRY(check_ptr(fn, "dh", dh));
     GQ_TRY(check_ptr(fn, "dx", dx));
-    GQ_TRY(check_ws(fn, "ws", ws, ws_bytes, need));
+    GQ_TRY(check_ws(fn, "ws", ws, ws_bytes, off[2]));
     uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u, times the scales' fractions
     const int64_t ldd = grad_ld(I);
     const gq::I8Mat gate{wq_gate, ld_gate, ws_gate}, upm{wq_up, ld_up, ws_up};
@@ -375,7 +383,7 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
                                                   H, N, (hipStream_t)stream)));
     const gq::I8GradPart parts[2] = {{gate, d}, {upm, d + ldd}};
     return launched(fn, gq::launch_grad_i8(parts, 2, true, 2 * ldd, dx, type, I, H, N,
-                                           (hipStream_t)stream));
+                                           (char *)ws + off[1], (hipStream_t)stream));
 }
 
 size_t gq_ffn_i8_workspace_bytes(int64_t T, int64_t H, int64_t I)

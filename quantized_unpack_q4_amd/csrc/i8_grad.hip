@@ -33,6 +33,9 @@ struct GradArgs {
     int nparts;
     int M, K, N; // d has zeros from M to the next multiple of 8
     int tiles_k, tiles_total;
+    int splits;     // runs of the sum, a workgroup each
+    float *partial; // their sums where there are several: [splits][N][ldp]
+    int64_t ldp;
 };
 
 template <bool BF16>
@@ -68,11 +71,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     constexpr int kD = 2 * BK * 128;      // byte offset of d in LDS
     static_assert(UN * NT == 8 * (BK / 4) && CX * 8 * NW == BN, "whole units and copies");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (BK + BN) * 128];
-    const TileWork work = tile_work(p.tiles_total, p.tiles_total);
+    const TileWork work = tile_work(p.tiles_total * p.splits, p.tiles_total * p.splits);
     if (work.tile < 0)
         return;
+    const int split = work.tile / p.tiles_total;
     int tk, tn;
-    tile_pos(work.tile, p.tiles_k, p.tiles_total / p.tiles_k, tk, tn);
+    tile_pos(work.tile % p.tiles_total, p.tiles_k, p.tiles_total / p.tiles_k, tk, tn);
     const int k0 = tk * BK, n0 = tn * BN;
     const int M = p.M, K = p.K;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -81,7 +85,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     const int r = lane & 31, h = lane >> 5;
     const int nv = min(p.N - n0, BN);
     const int nch = (M + 7) >> 3, nst = (nch + 7) >> 3; // chunks of 8 weight rows, stages of a part
-    const int total = p.nparts * nst;
+    // this workgroup's run of the stages of all parts
+    const int all = p.nparts * nst, first = (int)((int64_t)all * split / p.splits);
+    const int total = (int)((int64_t)all * (split + 1) / p.splits) - first;
 
     // d: copy i of this wave: rows 8 (CX wave + i) + lane / 8, slot lane % 8
     uint32_t doff[CX], dchk[CX];
@@ -92,9 +98,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         dchk[i] = (lane & 7) ^ swz8(row);
     }
     const uint32_t base = lds_addr(lds);
-    // stage t of the whole sum: stage st of part pt (past the last: the last again)
+    // stage t of the run: stage st of part pt (past the last: the last again)
     auto where = [&](int t, int &pt, int &st) {
-        t = min(t, total - 1);
+        t = first + min(t, total - 1);
         pt = t >= nst ? 1 : 0;
         st = t - pt * nst;
     };
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     };
     auto multiply = [&](int t, int s, Frag &f) {
         if constexpr (TAIL) { // gradients past M are zero (they may be anything)
-            const int st = t >= nst ? t - nst : t;
+            const int st = first + t >= nst ? first + t - nst : first + t;
             const bool none = 8 * st + 2 * s + h >= nch;
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
@@ -277,6 +283,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         const int n = 32 * (FN * wn + j) + r;
         if (n >= nv)
             break;
+        if (p.splits > 1) { // (rows hold a multiple of 16 columns)
+            float *sum = p.partial + ((int64_t)split * p.N + n0 + n) * p.ldp;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int k = k0 + 128 * wm + 32 * g + 16 * h;
+                if (k < K)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<float4_t *>(sum + k + 4 * c) =
+                            float4_t{acc[0][j][4 * g + c], acc[1][j][4 * g + c], acc[2][j][4 * g + c],
+                                     acc[3][j][4 * g + c]};
+            }
+            continue;
+        }
         uint16_t *out = p.dx + (int64_t)(n0 + n) * K;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -297,6 +317,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
                         out[k + c] = (uint16_t)(o[c >> 1] >> (16 * (c & 1)));
             }
         }
+    }
+}
+
+// The runs' sums added in run order and rounded once.
+template <bool BF16>
+__global__ __launch_bounds__(256) void grad_sum_kernel(const float *__restrict__ partial, int splits,
+                                                       int64_t ldp, uint16_t *__restrict__ dx, int K,
+                                                       int64_t N)
+{
+    const int64_t row4 = (K + 3) / 4, total = N * row4, step = (int64_t)gridDim.x * 256;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += step) {
+        const int64_t n = t / row4;
+        const int k = (int)(t - n * row4) * 4;
+        const float *s = partial + n * ldp + k;
+        float4_t v = *reinterpret_cast<const float4_t *>(s);
+        for (int i = 1; i < splits; ++i)
+            v += *reinterpret_cast<const float4_t *>(s + i * N * ldp);
+        mx_store4(dx, n * K + k, BF16 ? kBF16 : kF16, v, K - k, K % 4 == 0);
     }
 }
 
@@ -322,7 +360,7 @@ hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
     constexpr int BK = 128 * WM, BN = 32 * FN * WN;
     p.tiles_k = (p.K + BK - 1) / BK;
     p.tiles_total = p.tiles_k * ((p.N + BN - 1) / BN);
-    const dim3 grid(tile_grid(p.tiles_total, p.tiles_total)), block(64 * WM * WN);
+    const dim3 grid(tile_grid((int64_t)p.tiles_total * p.splits, (int64_t)p.tiles_total * p.splits)), block(64 * WM * WN);
     auto launch = [&](auto bf16, auto tail) {
         hipLaunchKernelGGL((grad_tile_kernel<decltype(bf16)::value, SPLIT, WM, WN, FN, decltype(tail)::value>),
                            grid, block, 0, st, p);
@@ -334,20 +372,47 @@ hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
     return hipGetLastError();
 }
 
-int grad_choice(int64_t K, int64_t N)
+struct GradTile {
+    int columns, rows, per_cu; // of a tile, and tiles a CU holds
+    double stage;              // us a stage takes
+};
+constexpr GradTile kTiles[] = {{256, 256, 1, 1.7}, {256, 128, 1, 1.2}, {128, 64, 3, 1.0}};
+
+struct GradPlan {
+    int tile, splits;
+};
+GradPlan grad_plan(int nparts, int64_t M, int64_t K, int64_t N)
 {
-    return N <= 64 ? 64 : (K + 255) / 256 * ((N + 255) / 256) < device_cus() ? 128 : 256;
+    constexpr int64_t kCus = 256;
+    const int64_t stages = nparts * ((M + 63) / 64);
+    GradPlan best{};
+    double least = 1e30;
+    for (int i = 0; i < 3; ++i) {
+        const GradTile &t = kTiles[i];
+        const int64_t tiles = (K + t.columns - 1) / t.columns * ((N + t.rows - 1) / t.rows);
+        for (int s = 1; s <= 16 && s <= stages; ++s) {
+            const int64_t rounds = (tiles * s + kCus * t.per_cu - 1) / (kCus * t.per_cu);
+            double us = (double)rounds * ((double)((stages + s - 1) / s) * t.stage + 4.0);
+            if (s > 1)
+                us += 3.0 + (double)(s * N * K) * 8.0 / 4e6;
+            if (us < least)
+                least = us, best = {i, s};
+        }
+    }
+    return best;
 }
 
 template <bool SPLIT>
-hipError_t launch_grad(const GradArgs &p, int type, hipStream_t st)
+hipError_t launch_grad(const GradArgs &p, int tile, int type, hipStream_t st)
 {
-    switch (grad_choice(p.K, p.N)) {
-    case 64: return launch_grad_tiles<SPLIT, 1, 2, 1>(p, type, st);
-    case 128: return launch_grad_tiles<SPLIT, 1, 4, 1>(p, type, st);
-    default: return launch_grad_tiles<SPLIT, 2, 4, 2>(p, type, st);
+    switch (tile) {
+    case 0: return launch_grad_tiles<SPLIT, 2, 4, 2>(p, type, st);
+    case 1: return launch_grad_tiles<SPLIT, 2, 4, 1>(p, type, st);
+    default: return launch_grad_tiles<SPLIT, 1, 2, 1>(p, type, st);
     }
 }
+
+int64_t partial_ld(int64_t K) { return (K + 15) / 16 * 16; }
 
 } // namespace
 
@@ -360,9 +425,17 @@ hipError_t launch_align_rows(const uint16_t *d, int64_t ldd, uint16_t *out, int6
     return hipGetLastError();
 }
 
-hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
-                          uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, hipStream_t st)
+size_t grad_partial_bytes(int nparts, int64_t M, int64_t K, int64_t N)
 {
+    const int splits = grad_plan(nparts, M, K, N).splits;
+    return splits > 1 ? (size_t)splits * N * partial_ld(K) * 4 : 0;
+}
+
+hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
+                          uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, void *partial,
+                          hipStream_t st)
+{
+    const GradPlan plan = grad_plan(nparts, M, K, N);
     GradArgs p{};
     p.part[0] = parts[0];
     p.part[1] = parts[nparts - 1];
@@ -372,7 +445,21 @@ hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64
     p.M = (int)M;
     p.K = (int)K;
     p.N = (int)N;
-    return split ? launch_grad<true>(p, type, st) : launch_grad<false>(p, type, st);
+    p.splits = plan.splits;
+    p.partial = (float *)partial;
+    p.ldp = partial_ld(K);
+    const hipError_t e = split ? launch_grad<true>(p, plan.tile, type, st)
+                               : launch_grad<false>(p, plan.tile, type, st);
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    const dim3 grid((unsigned)std::min((N * ((K + 3) / 4) + 255) / 256, (int64_t)1 << 14)), block(256);
+    if (type == kBF16)
+        hipLaunchKernelGGL(grad_sum_kernel<true>, grid, block, 0, st, p.partial, p.splits, p.ldp, dx,
+                           (int)K, N);
+    else
+        hipLaunchKernelGGL(grad_sum_kernel<false>, grid, block, 0, st, p.partial, p.splits, p.ldp, dx,
+                           (int)K, N);
+    return hipGetLastError();
 }
 
 } // namespace gq

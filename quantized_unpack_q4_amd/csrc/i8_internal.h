@@ -55,8 +55,12 @@ struct I8GradPart {
     I8Mat w;
     const uint16_t *d;
 };
+// The sum may be cut into runs, whose sums then go through `partial`, this many bytes (zero: one
+// run).
+size_t grad_partial_bytes(int nparts, int64_t M, int64_t K, int64_t N);
 hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
-                          uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, hipStream_t st);
+                          uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, void *partial,
+                          hipStream_t st);
 
 // Rows of M 16-bit values, ldd apart, to rows ldo apart (a multiple of 8), zeros behind them.
 hipError_t launch_align_rows(const uint16_t *d, int64_t ldd, uint16_t *out, int64_t ldo, int64_t M,

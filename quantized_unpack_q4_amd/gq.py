@@ -157,11 +157,12 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = st
             f.argtypes = args
-        for name in ("gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8_workspace_bytes",
-                     "gq_gemm_i8_backward_workspace_bytes"):
+        for name in ("gq_gated_i8_backward_workspace_bytes", "gq_ffn_i8_workspace_bytes"):
             f = getattr(L, name)
             f.restype = sz
             f.argtypes = [i64, i64, i64]
+        L.gq_gemm_i8_backward_workspace_bytes.restype = sz
+        L.gq_gemm_i8_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
         L.gq_gemv_i8_workspace_bytes.restype = sz
         L.gq_gemv_i8_workspace_bytes.argtypes = [i64, i64]
         L.gq_last_error.restype = ctypes.c_char_p
@@ -465,8 +466,8 @@ def gq_gemm_i8(wq, ldw, ws, xq, ldx, xs, y, y_type, M, K, N, stream=None):
                             N, _stream(stream)))
 
 
-def gq_gemm_i8_backward_workspace_bytes(M, N, ldd) -> int:
-    return int(lib().gq_gemm_i8_backward_workspace_bytes(M, N, ldd))
+def gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd) -> int:
+    return int(lib().gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd))
 
 
 def gq_gemm_i8_backward(wq, ldw, ws, dy, ldd, dx, dtype, M, K, N, wsp=None, ws_bytes=None,
@@ -954,8 +955,7 @@ def gemm_i8(wq, ws, xq, xs, dtype=None, out=None, stream=None):
 def gemm_i8_backward(wq, ws, dy, wsp=None, out=None, stream=None):
     """dX [N][K] = dY [N][M] * W in dY's dtype (float16 or bfloat16): the gradient of the values
     of X for a gradient dY of gemm_i8's (or gemv_i8's) result; rows of dY contiguous, any
-    distance apart (where they do not all start 16-byte aligned, they are copied into a
-    workspace, wsp or a new one)."""
+    distance apart.  Some sizes take a workspace, wsp or a new one."""
     _, dev = _mx_enter("dY", dy)
     wa, ldw, wsa, M, K = _i8_matrix("W", wq, ws, dev)
     code = _mx_dtype(dy.dtype, f32=False)
@@ -963,7 +963,7 @@ def gemm_i8_backward(wq, ws, dy, wsp=None, out=None, stream=None):
     if MD != M:
         raise ValueError("dY has rows of %d values, expected %d" % (MD, M))
     dx = _mx_new((N, K), dy.dtype, dy, stream) if out is None else out
-    need = lib().gq_gemm_i8_backward_workspace_bytes(M, N, ldd)
+    need = lib().gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd)
     _check(lib().gq_gemm_i8_backward(wa, ldw, wsa, dy.data_ptr(), ldd,
                                      _mx_addr("out", dx, dev, dy.dtype, (N, K)), code, M, K, N,
                                      *_i8_wsp("wsp", wsp, need, dy, dev, stream),

@@ -114,16 +114,19 @@ def test_gemm_backward_refusals(L):
 
     from quantized_unpack_q4_amd import gq
     size = gq.gq_gemm_i8_backward_workspace_bytes
-    assert size(8, 2, 16) == 0 and size(8, 1, 3) == 0 and size(8, 0, 8) == 0
-    assert size(8, 2, 9) == 2 * 8 * 2 and size(9, 2, 16) == 2 * 16 * 2 and size(9, 1, 0) == 32
-    assert size(8, 2, 7) == 0 and "ldd = 7" in gq.last_error()
+    # (8 weight rows are one run of the sum)
+    assert size(8, 64, 2, 16) == 0 and size(8, 64, 1, 3) == 0 and size(8, 64, 0, 8) == 0
+    need = size(8, 64, 2, 9)
+    assert need >= 2 * 8 * 2 and size(9, 64, 2, 16) >= 2 * 16 * 2 and size(9, 64, 1, 0) >= 32
+    assert size(4096, 4096, 130, 4096) % (130 * 4096 * 4) == 0
+    assert size(8, 64, 2, 7) == 0 and "ldd = 7" in gq.last_error()
 
     def call(wq=P, ldw=64, ws=P, dy=P, ldd=8, dx=P, t=F16, M=8, K=64, N=2, wsp=None, n=0):
         return f(wq, ldw, ws, dy, ldd, dx, t, M, K, N, wsp, n, None)
 
-    refused(L, call(ldd=9), "GQ_EWORKSPACE", "wsp", "32")
-    refused(L, call(ldd=9, wsp=P, n=31), "GQ_EWORKSPACE", "32")
-    refused(L, call(ldd=9, wsp=BAD, n=32), "GQ_EALIGN", "wsp")
+    refused(L, call(ldd=9), "GQ_EWORKSPACE", "wsp", str(need))
+    refused(L, call(ldd=9, wsp=P, n=need - 1), "GQ_EWORKSPACE", str(need))
+    refused(L, call(ldd=9, wsp=BAD, n=need), "GQ_EALIGN", "wsp")
 
     refused(L, call(t=F32), "GQ_EINVAL", "type = 0")
     refused(L, call(M=0), "GQ_EINVAL", "M = 0")
