@@ -3,10 +3,12 @@
 // A row's codes are q = 127 x / max|x| rounded to the nearest whole number, halves to even,
 // decided as if in exact arithmetic: x = max|x| / 2 is a tie in every row (63.5), so a
 // quotient rounded first would fall on either side.  The quotient in binary32 is off by less
-// than 127 * 2^-23 < 2^-16; only where it lies within 2^-12 of a half (one value in 2000) is
-// it formed again in binary64, where 127 x is exact and the quotient of two binary32
-// numbers that is not a half itself lies 2^-33 or more from one.
+// than 127 * 2^-23 < 2^-16; only where it lies within 2^-15 of a half (one value in 16000, and
+// the ties of short types) is 254 x compared with the odd multiple of max|x| that the half
+// stands for.
 #pragma once
+
+#include <type_traits>
 
 #include "gq_device.h"
 #include "i8_internal.h"
@@ -36,7 +38,7 @@ __device__ __forceinline__ uint32_t load_dword(const int8_t *base, uint32_t off)
 
 // What quantising a row takes: its largest magnitude, the scale (NaN for a row with an
 // infinity or a NaN, whose codes are zero) and the factor of the quotient; r < 0 for rows of
-// very small values, where 127 / max could be infinite: all their codes come from binary64.
+// very small values, where 127 / max could be infinite: their codes take the exact way.
 struct I8Row {
     float top, s, r;
     __device__ __forceinline__ explicit I8Row(uint32_t max_bits)
@@ -56,6 +58,33 @@ __device__ __forceinline__ float i8_load(const void *x, int64_t i)
         return reinterpret_cast<const float *>(x)[i];
     const uint32_t u = reinterpret_cast<const uint16_t *>(x)[i];
     return TYPE == kBF16 ? __builtin_bit_cast(float, u << 16) : half_to_float(u);
+}
+
+// A binary32 value as it stands: without this the compiler may merge its last operation and the
+// rounding to binary16 into one instruction with one rounding, and results would depend on
+// which kernel, and which type, they were formed in.
+__device__ __forceinline__ float as_is(float v)
+{
+    asm("" : "+v"(v));
+    return v;
+}
+
+// The largest of a wave's values, in a scalar register: six dependent vector instructions, where
+// exchanges through LDS would take six of its latencies.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
+                                                         decltype(rows)::value, 0xF, false));
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});  // lane ^ 1
+    step(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});  // lane ^ 2
+    step(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{}); // mirrored in 8
+    step(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{}); // mirrored in 16
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{}); // rows 0, 2 to 1, 3
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{}); // rows 0, 1 to 2, 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // Eight consecutive values of a row (any alignment), of which n exist; the others are zero.
@@ -118,6 +147,22 @@ struct I8Load8<kF32> {
     __device__ __forceinline__ float value(int j) const { return v[j]; }
 };
 
+// The code of x, exactly.  The quotient lies between two halves of codes; h is the one nearer to
+// it, and 254 x - 2 h top decides on which side of h it is: 2 h is odd and at most 253, so
+// 2 h top is p + e of two binary32 numbers, and 254 x - p is exact where the two are close
+// (elsewhere its sign is).  x and top are scaled so that none of it overflows or vanishes.
+__device__ __forceinline__ int i8_code_exact(float x, float top)
+{
+    const float f = top < 0x1p-60f ? 0x1p100f : top > 1.0f ? 0x1p-16f : 1.0f;
+    x *= f;
+    top *= f;
+    const float t = x * (127.0f / top), q = rintf(t);
+    const float h = q + copysignf(0.5f, t - q), odd = 2.0f * h;
+    const float p = as_is(odd * top), e = fmaf(odd, top, -p), d = fmaf(254.0f, x, -p) - e;
+    const int lo = (int)(h - 0.5f); // h lies between lo and lo + 1
+    return d > 0.0f ? lo + 1 : d < 0.0f ? lo : lo + (lo & 1);
+}
+
 // Eight codes of a row, packed.  1.5 * 2^23 added to a quotient leaves the nearest whole number
 // in the low bits, its lowest byte the code.
 template <int TYPE>
@@ -132,10 +177,10 @@ __device__ __forceinline__ uint2 i8_codes8(const I8Load8<TYPE> &v, const I8Row &
         off = fmaxf(off, fabsf(t - (m - magic)));
         b[j] = __builtin_bit_cast(uint32_t, m);
     }
-    if (__builtin_expect(off > 0.5f - 0x1p-12f || row.r < 0.0f, 0)) {
+    if (__builtin_expect(off > 0.5f - 0x1p-15f || row.r < 0.0f, 0)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            b[j] = (uint32_t)(int)rint(127.0 * (double)v.value(j) / (double)row.top);
+            b[j] = (uint32_t)i8_code_exact(v.value(j), row.top);
     }
     const uint32_t keep = row.r == 0.0f ? 0u : ~0u; // zero rows, and those with NaN
     auto pack = [&](int j) {
@@ -144,15 +189,6 @@ __device__ __forceinline__ uint2 i8_codes8(const I8Load8<TYPE> &v, const I8Row &
         return (lo | hi) & keep;
     };
     return make_uint2(pack(0), pack(4));
-}
-
-// A binary32 value as it stands: without this the compiler may merge its last operation and the
-// rounding to binary16 into one instruction with one rounding, and results would depend on
-// which kernel, and which type, they were formed in.
-__device__ __forceinline__ float as_is(float v)
-{
-    asm("" : "+v"(v));
-    return v;
 }
 
 // act(z) = z sigmoid(p(z)), p = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3) (GELU's tanh

@@ -67,9 +67,7 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
                 v.load(p.x, (int64_t)b * K + k0 + k, min(cols - k, 8));
                 m = max(m, v.max_bits());
             }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1)
-                m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+            m = wave_max(m);
             if (lane == 0)
                 part[b][wave] = m;
         }
