@@ -565,9 +565,9 @@ gq_status gq_dequant_i8(const int8_t *q, int64_t ldq, const float *s, void *out,
 /* int8 matrix-vector product for 1 <= B <= GQ_GEMV_MAX_BATCH activation rows, quantised on the
  * way as by gq_quantize_i8 (the same results as that and gq_gemm_i8, bit for bit):
  *   y[b][r] = sum_k w[r][k] * v(x)[b][k].
- * Few values (B*K <= 16384) are quantised by the workgroups that multiply them, in one launch
- * and without a workspace (wsp may be NULL); more are quantised once, by a launch before, into
- * wsp: at least gq_gemv_i8_workspace_bytes(K, B) bytes, 16-byte aligned, contents on entry
+ * One row of K <= 16384, two of K <= 8192 and up to four of K <= 4096 are quantised by the
+ * workgroups that multiply them, in one launch and without a workspace (wsp may be NULL); more
+ * are quantised once, by a launch before, into wsp: at least gq_gemv_i8_workspace_bytes(K, B) bytes, 16-byte aligned, contents on entry
  * ignored; not to be in use by another call while this one runs.
  * x: [B][K] and y: [B][M], both of `type` (any gq_dtype).  Requires K <= 131071, M <= 2^26,
  * ldw <= 2^22. */

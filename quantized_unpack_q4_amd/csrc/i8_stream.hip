@@ -38,16 +38,16 @@ __device__ __forceinline__ int4v mfma16_i8(uint4 a, uint4 b, int4v c)
 
 // Bytes of LDS for codes: rows of a run are 16 bytes further apart than the run is long, so
 // that 16 rows' reads touch distinct banks.
-constexpr int64_t codes_bytes(int W, int64_t B, int64_t run) { return W * B * (run + 16); }
+constexpr int codes_bytes(int W, int B, int run) { return W * B * (run + 16); }
 
 template <int SRC, bool PAIR, int W, int LDSB>
 __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 {
-    constexpr int P = PAIR ? 2 : 1, U = 8;
+    constexpr int P = PAIR ? 2 : 1, U = 8; // U steps loaded at once
     constexpr bool FLOATS = SRC != kCodes;
     __shared__ __attribute__((aligned(16))) uint8_t codes[FLOATS ? LDSB : 16];
-    __shared__ uint32_t part[16][W];
-    __shared__ float xscale[16];
+    __shared__ uint32_t part[4][W];
+    __shared__ float xscale[4];
     __shared__ int4v red[W][P][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -59,84 +59,108 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
     const int pitch = p.run + 16;
     uint8_t *mine = codes + (FLOATS ? wave * B * pitch : 0);
 
+    const int tiles = (M + 15) >> 4;
+    const int xr = min(r, B - 1);
+    const int8_t *xp = FLOATS ? nullptr : p.xc.q + xr * p.xc.ld;
+    // weights (and codes of activations) of U steps from s0
+    struct Batch {
+        uint4 a[P][U], x[FLOATS ? 1 : U];
+    };
+    auto load = [&](int tile, int s0, Batch &t) {
+        const int64_t wr = min(16 * tile + r, M - 1);
+        const int8_t *wp[2] = {p.w.q + wr * p.w.ld, PAIR ? p.w2.q + wr * p.w2.ld : nullptr};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s0 + u >= steps)
+                break;
+            const int ch = min((k0 >> 4) + 4 * (s0 + u) + q, lastc);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                t.a[i][u] = ld16(wp[i] + 16 * ch);
+            if constexpr (!FLOATS)
+                t.x[u] = ld16(xp + 16 * ch);
+        }
+    };
+    Batch now;
     if constexpr (FLOATS) {
-        for (int b = 0; b < B; ++b) {
-            uint32_t m = 0;
-            for (int k = 8 * lane; k < cols; k += 512) {
-                I8Load8<SRC> v;
-                v.load(p.x, (int64_t)b * K + k0 + k, min(cols - k, 8));
-                m = max(m, v.max_bits());
-            }
-            m = wave_max(m);
+        // All values, before the first weights, which then come while they are quantised: two
+        // pieces of 512 columns of one or two rows, or one of up to four.
+        const bool two = B <= 2;
+        const int pieces = two ? (p.run > 512 ? 2 * B : 2 * B - 1) : B; // (the last may be empty)
+        I8Load8<SRC> x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= pieces)
+                break;
+            const int b = two ? i >> 1 : i, c = 8 * lane + (two ? 512 * (i & 1) : 0);
+            x[i].load(p.x, (int64_t)b * K + k0 + c, max(min(cols - c, 8), 0));
+        }
+        load(blockIdx.x, 0, now);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = i < pieces ? wave_max(x[i].max_bits()) : 0;
             if (lane == 0)
-                part[b][wave] = m;
+                part[i][wave] = m;
         }
         __syncthreads();
         uint32_t m = 0;
-        if (lane < B)
+        if (lane < 4)
 #pragma unroll
             for (int i = 0; i < W; ++i)
                 m = max(m, part[lane][i]);
-        const I8Row row(m); // lane b: row b
-        if (wave == 0 && lane < B)
-            xscale[lane] = row.s;
-        const int nb = 8 * steps; // blocks of 8 columns of a row
-        for (int b = 0; b < B; ++b) {
-            const I8Row rb(__shfl(row.top, b, 64), __shfl(row.s, b, 64), __shfl(row.r, b, 64));
-            for (int c = lane; c < nb; c += 64) {
-                I8Load8<SRC> v;
-                v.load(p.x, (int64_t)b * K + k0 + 8 * c, max(min(cols - 8 * c, 8), 0));
-                *reinterpret_cast<uint2 *>(mine + b * pitch + 8 * c) = i8_codes8(v, rb);
-            }
+        if (two)
+            m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+        const I8Row row(m); // lane i: piece i's
+        if (wave == 0 && lane < 4)
+            xscale[two ? lane >> 1 : lane] = row.s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= pieces)
+                break;
+            const I8Row rb(__shfl(row.top, i, 64), __shfl(row.s, i, 64), __shfl(row.r, i, 64));
+            const int b = two ? i >> 1 : i, c = 8 * lane + (two ? 512 * (i & 1) : 0);
+            if (c < 64 * steps)
+                *reinterpret_cast<uint2 *>(mine + b * pitch + c) = i8_codes8(x[i], rb);
         }
         lds_wave_order();
     }
 
-    const int tiles = (M + 15) >> 4;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int m0 = 16 * tile;
-        const int64_t wr = min(m0 + r, M - 1);
-        const int8_t *wp[2] = {p.w.q + wr * p.w.ld, PAIR ? p.w2.q + wr * p.w2.ld : nullptr};
-        const int xr = min(r, B - 1);
-        const int8_t *xp = FLOATS ? nullptr : p.xc.q + xr * p.xc.ld;
         int4v acc[P];
 #pragma unroll
         for (int i = 0; i < P; ++i)
             acc[i] = int4v{0, 0, 0, 0};
         for (int s0 = 0; s0 < steps; s0 += U) {
-            uint4 a[P][U], xv[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int ch = min((k0 >> 4) + 4 * (s0 + u) + q, lastc);
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    a[i][u] = ld16(wp[i] + 16 * ch);
-                if (!FLOATS)
-                    xv[u] = ld16(xp + 16 * ch);
-            }
+            if (s0 > 0 || !FLOATS)
+                load(tile, s0, now);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (s0 + u >= steps)
                     break;
+                uint4 xv;
                 if constexpr (FLOATS) {
-                    xv[u] = ld16(mine + xr * pitch + 64 * (s0 + u) + 16 * q);
+                    xv = ld16(mine + xr * pitch + 64 * (s0 + u) + 16 * q);
                 } else {
+                    xv = now.x[u];
                     const int left = K - (k0 + 64 * (s0 + u) + 16 * q); // codes past K are zero
                     if (__builtin_expect(left < 16, 0)) {
-                        uint32_t t[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+                        uint32_t t[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int n = min(max(left - 4 * j, 0), 4);
                             t[j] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
                         }
-                        xv[u] = make_uint4(t[0], t[1], t[2], t[3]);
+                        xv = make_uint4(t[0], t[1], t[2], t[3]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < P; ++i)
-                    acc[i] = mfma16_i8(a[i][u], xv[u], acc[i]);
+                    acc[i] = mfma16_i8(now.a[i][u], xv, acc[i]);
             }
         }
+        if (FLOATS && tile + (int)gridDim.x < tiles) // while this tile's sums are joined
+            load(tile + gridDim.x, 0, now);
 #pragma unroll
         for (int i = 0; i < P; ++i)
             red[wave][i][lane] = acc[i];
@@ -165,18 +189,14 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 
 // Sixteen waves where K is long enough to keep eight waiting for their weights.
 constexpr int64_t kLongK = 8192;
-// Values a workgroup quantises itself.
-constexpr int64_t kFused = 16384;
 
 template <int SRC, bool PAIR, int W>
 hipError_t launch_waves(I8StreamArgs p, int64_t grid, hipStream_t st)
 {
-    // a run is at most K / W + 64 columns, and where K is long one row is quantised at most
-    constexpr int B = W == 8 ? 16 : 1;
-    constexpr int LDSB = SRC == kCodes ? 16 : (int)(kFused + W * B * (64 + 16));
-    static_assert(W == 8 || 2 * kLongK >= kFused, "one row");
+    // codes of up to four rows: see i8_fused
+    constexpr int LDSB = SRC == kCodes ? 16 : std::max(codes_bytes(W, 4, 512), codes_bytes(W, 1, 1024));
     p.run = ((p.K + W - 1) / W + 63) / 64 * 64;
-    if (SRC != kCodes && codes_bytes(W, p.B, p.run) > LDSB)
+    if (SRC != kCodes && (!i8_fused(p.K, p.B) || codes_bytes(W, p.B, p.run) > LDSB))
         return hipErrorInvalidValue;
     hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, LDSB>), dim3((unsigned)grid), dim3(64 * W), 0, st,
                        p);
@@ -187,7 +207,11 @@ template <int SRC, bool PAIR>
 hipError_t launch_stream(const I8StreamArgs &p, hipStream_t st)
 {
     const int64_t tiles = ((int64_t)p.M + 15) / 16;
-    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, tiles, st) : launch_waves<SRC, PAIR, 8>(p, tiles, st);
+    // Floats: as many workgroups as the CUs hold at once, which quantise once for all of their
+    // tiles (14336 x 4096, batch 4: 17 us, with a workgroup a tile 24).  Codes: one a tile.
+    const int64_t most = SRC == kCodes ? tiles : (p.K > kLongK ? 1 : 2) * device_cus();
+    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, std::min(tiles, most), st)
+                        : launch_waves<SRC, PAIR, 8>(p, std::min(tiles, most), st);
 }
 
 template <bool PAIR>
@@ -214,7 +238,13 @@ I8StreamArgs args(I8Mat w, I8Mat w2, void *y, int type, int act, int64_t M, int6
 
 } // namespace
 
-bool i8_fused(int64_t K, int64_t B) { return B <= 16 && B * K <= kFused; }
+// What four pieces of 512 columns for each of eight (one row: sixteen) waves hold.  More rows
+// are better quantised once: four rows of 4096 take 17 us against 14336 weight rows, 18.6 with
+// codes from a launch before, which sixteen rows of 1024, one after another, took too.
+bool i8_fused(int64_t K, int64_t B)
+{
+    return B == 1 ? K <= 2 * kLongK : B == 2 ? K <= kLongK : B <= 4 && K <= kLongK / 2;
+}
 
 hipError_t launch_gemv_i8(I8Mat w, const void *x, void *y, int type, int64_t M, int64_t K, int B,
                           hipStream_t st)

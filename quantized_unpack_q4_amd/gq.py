@@ -920,8 +920,8 @@ def dequant_i8(q, s, dtype=None, out=None, stream=None):
 
 def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     """y [B][M] = x [B][K] * W^T in x's dtype (float32, float16 or bfloat16) for int8 W [M][K],
-    1 <= B <= 16, x quantised per row on the way (from 16384 values on in a workspace, wsp or a
-    new one)."""
+    1 <= B <= 16, x quantised per row on the way (more than a few rows in a workspace, wsp or
+    a new one)."""
     _, dev = _mx_enter("x", x)
     qa, ld, sa, M, K = _i8_matrix("W", wq, ws, dev)
     code = _mx_dtype(x.dtype)

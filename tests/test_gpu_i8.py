@@ -159,8 +159,9 @@ def test_gemm(M, K, N, t):
 
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("M,K", [(1, 1), (15, 16), (16, 17), (100, 64), (33, 127), (260, 1000),
-                                 (70, 4096), (4100, 130), (40, 14336), (37, 9999), (20, 70001)])
-@pytest.mark.parametrize("B", [1, 2, 3, 5, 8, 16])
+                                 (70, 4096), (4100, 130), (40, 14336), (37, 9999), (20, 70001),
+                                 (50, 4097), (33, 8192), (9010, 8193), (17, 16384), (16, 16385)])
+@pytest.mark.parametrize("B", [1, 2, 3, 4, 5, 8, 16])
 def test_gemv(M, K, B, t):
     wq, ws = i8.rows(12, M, K, -128, 127)
     x, x64 = floats(13, B, K, t, 2.0)

@@ -77,7 +77,9 @@ def test_gemv_refusals(L):
     refused(L, call(ws=BAD), "GQ_EALIGN", "ws")
     refused(L, call(x=None), "GQ_EINVAL", "x is NULL")
     from quantized_unpack_q4_amd import gq
-    assert gq.gq_gemv_i8_workspace_bytes(1024, 16) == 0
+    for K, B in ((16384, 1), (8192, 2), (4096, 3), (4096, 4)):
+        assert gq.gq_gemv_i8_workspace_bytes(K, B) == 0
+        assert gq.gq_gemv_i8_workspace_bytes(K + 1, B) > B * (K + 1)
     need = gq.gq_gemv_i8_workspace_bytes(1025, 16)
     assert need >= 16 * (1040 + 4)
     refused(L, call(K=1025, ldw=1040, B=16), "GQ_EWORKSPACE", str(need))
