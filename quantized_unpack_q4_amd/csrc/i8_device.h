@@ -193,8 +193,8 @@ __device__ __forceinline__ uint2 i8_codes8(const I8Load8<TYPE> &v, const I8Row &
 
 // act(z) = z sigmoid(p(z)), p = z (SiLU) or 2 sqrt(2/pi) (z + 0.044715 z^3) (GELU's tanh
 // form: 0.5 (1 + tanh(p / 2)) = sigmoid(p)), and its derivative
-// sigmoid(p) + z p'(z) sigmoid(p) (1 - sigmoid(p)).  e^-p may overflow: the sigmoid is then
-// zero, as it should be; z in the derivative's second term is cut at 64, where that term is
+// sigmoid(p) + z p'(z) sigmoid(p) (1 - sigmoid(p)).  The reciprocal is the instruction's, off by
+// a unit in the last place.  e^-p may overflow: the sigmoid is then zero, as it should be; z in the derivative's second term is cut at 64, where that term is
 // long zero, so that no zero meets an infinity.
 struct Gate {
     float a, da;
@@ -206,12 +206,12 @@ __device__ __forceinline__ float gate_poly(float z, int act)
 }
 __device__ __forceinline__ float gated_value(float g, float u, int act)
 {
-    return as_is(g / (1.0f + __expf(-gate_poly(g, act))) * u);
+    return as_is(g * __builtin_amdgcn_rcpf(1.0f + __expf(-gate_poly(g, act))) * u);
 }
 __device__ __forceinline__ Gate gate_grad(float z, int act)
 {
     constexpr float c = 1.5957691216057308f, a = 0.044715f;
-    const float sig = 1.0f / (1.0f + __expf(-gate_poly(z, act)));
+    const float sig = __builtin_amdgcn_rcpf(1.0f + __expf(-gate_poly(z, act)));
     const float zc = fminf(fmaxf(z, -64.0f), 64.0f);
     const float dp = act == kSilu ? 1.0f : c * fmaf(3.0f * a * zc, zc, 1.0f);
     return {z * sig, fmaf(zc * dp, sig * (1.0f - sig), sig)};
@@ -234,10 +234,15 @@ __device__ __forceinline__ float scale_pow2(float s)
     const uint32_t e = __builtin_bit_cast(uint32_t, s) & 0x7f800000u;
     return __builtin_bit_cast(float, min(e + 0x00800000u, 0x7f000000u));
 }
-__device__ __forceinline__ float scale_fraction(float s) { return s * (1.0f / scale_pow2(s)); }
+__device__ __forceinline__ float scale_fraction(float s)
+{
+    const uint32_t e = __builtin_bit_cast(uint32_t, scale_pow2(s)) >> 23;
+    return __builtin_amdgcn_ldexpf(s, 127 - (int)e);
+}
 
-// Four consecutive 16-bit values from element i (any alignment), of which n exist.
-__device__ __forceinline__ float4_t load4(const uint16_t *x, int64_t i, int64_t n, int type)
+// Four consecutive 16-bit values from element i (any alignment), of which n exist, as they lie,
+// and as binary32.
+__device__ __forceinline__ uint2 load4(const uint16_t *x, int64_t i, int64_t n)
 {
     uint2 u = make_uint2(0, 0);
     if (n >= 4) {
@@ -250,6 +255,10 @@ __device__ __forceinline__ float4_t load4(const uint16_t *x, int64_t i, int64_t 
         if (n > 2)
             u.y = x[i + 2];
     }
+    return u;
+}
+__device__ __forceinline__ float4_t values4(uint2 u, int type)
+{
     if (type == kBF16)
         return {__builtin_bit_cast(float, u.x << 16), __builtin_bit_cast(float, u.x & 0xffff0000u),
                 __builtin_bit_cast(float, u.y << 16), __builtin_bit_cast(float, u.y & 0xffff0000u)};

@@ -45,23 +45,19 @@ __device__ __forceinline__ int16v mfma_i8(uint4 a, uint4 b, int16v c)
                                                  __builtin_bit_cast(int4v, b), c, 0, 0, 0);
 }
 
-template <int WM, int WN, int FM, int FN, int NB>
+// Groups of 8 weight rows that a wave stores at once: all of its rows, or a fragment's where two
+// results are held.
+constexpr int store_groups(int MODE, int FM) { return MODE == kPlain ? 4 * FM : MODE == kGated ? 2 * FM : 4; }
+
+// After the stages LDS holds the waves' scratch for storing and, per weight row, the scales of
+// both matrices and their fractions.
+constexpr int scratch_bytes(int MODE, int NW, int FM) { return NW * store_scratch(store_groups(MODE, FM), 4); }
+
+template <int MODE, int WM, int WN, int FM, int FN, int NB>
 constexpr int i8_lds_bytes()
 {
-    return std::max(NB * (32 * FM * WM + 32 * FN * WN) * 128, WM * WN * store_scratch(4 * FM, 4));
-}
-
-// The scales of weight rows m .. m + 3, of which those below M exist.
-__device__ __forceinline__ float4_t scales4(const float *s, int64_t m, int64_t M)
-{
-    if (m + 4 <= M)
-        return *reinterpret_cast<const float4_t *>(s + m);
-    float4_t v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (m + i < M)
-            v[i] = s[m + i];
-    return v;
+    constexpr int BM = 32 * FM * WM;
+    return std::max(NB * (BM + 32 * FN * WN) * 128, scratch_bytes(MODE, WM * WN, FM) + 4 * BM * 4);
 }
 
 // The tile of weight rows m0 .. (of each matrix) and activation rows n0 ..: NB stages in LDS,
@@ -74,7 +70,7 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
     constexpr bool PAIR = MODE != kPlain;
     constexpr int BW = PAIR ? BM / 2 : BM, FW = PAIR ? FM / 2 : FM; // rows, fragments of a matrix
     // one wave a SIMD: the compiler keeps the accumulators in the other register file
-    constexpr bool AGPR = NW <= 4 && i8_lds_bytes<WM, WN, FM, FN, NB>() > (80 << 10);
+    constexpr bool AGPR = NW <= 4 && i8_lds_bytes<MODE, WM, WN, FM, FN, NB>() > (80 << 10);
     static_assert(NC * 8 * NW == BR && BW % 8 == 0 && (!PAIR || FM % 2 == 0), "whole copies, pairs");
     const int M = p.M, K = p.K;
     const uint32_t ldw = (uint32_t)p.w.ld, ldw2 = (uint32_t)(PAIR ? p.w2.ld : p.w.ld), ldx = (uint32_t)p.x.ld;
@@ -208,11 +204,30 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
     }
     wait_copies<0>();
 
+    // per weight row of the tile: the scales and, for gradients, their fractions
+    constexpr int G = store_groups(MODE, FM);
+    float *const sc = reinterpret_cast<float *>(lds + scratch_bytes(MODE, NW, FM));
+    for (int i = tid; i < BW; i += 64 * NW) {
+        const bool in = m0 + i < M; // (rows past the last: zeros, as their results then are)
+        const float ws = in ? p.w.s[m0 + i] : 0.0f;
+        sc[i] = ws;
+        if constexpr (PAIR) {
+            const float us = in ? p.w2.s[m0 + i] : 0.0f;
+            sc[BW + i] = us;
+            if constexpr (MODE == kGrads) {
+                sc[2 * BW + i] = scale_fraction(ws);
+                sc[3 * BW + i] = scale_fraction(us);
+            }
+        }
+    }
+    __syncthreads();
+
     // element v of an accumulator: weight row 8 (v / 4) + 4 h + v % 4, activation row r
-    const int64_t m = m0 + 32 * FW * wm;
+    const int mw = 32 * FW * wm; // the wave's first row in the tile
+    const int64_t m = m0 + mw;
     if (m >= M)
         return;
-    uint8_t *scr = lds + wave * store_scratch(4 * FM, 4);
+    uint8_t *scr = lds + wave * store_scratch(G, 4);
     auto scaled4 = [&](int i, int j, int v4, float4_t ws, float xs) {
         float4_t v;
 #pragma unroll
@@ -220,18 +235,17 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
             v[c] = i8_scaled(acc[i][j][4 * v4 + c], ws[c], xs);
         return v;
     };
-    // weight rows of a store: all of the wave's, or a fragment's where two results are held
-    constexpr int G = MODE == kGrads ? 4 : 4 * FW;
     // (gradients past the last row, up to a multiple of 8, are stored: zeros, as their dh is)
     const int64_t end = MODE == kGrads ? (M + 7) / 8 * 8 : M;
     auto store = [&](const float4_t(&v)[G], void *y, int64_t n, int left, int64_t m) {
-        if (p.type == kF32)
+        if (MODE != kGrads && p.type == kF32)
             store_rows<kF32>(scr, y, n, left, m, end, v, p.ldy);
         else if (p.type == kF16)
             store_rows<kF16>(scr, y, n, left, m, end, v, p.ldy);
         else
             store_rows<kBF16>(scr, y, n, left, m, end, v, p.ldy);
     };
+    const bool full = m + 32 * FW <= M; // (uniform)
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const int n = 32 * (FN * wn + j);
@@ -239,30 +253,44 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
             break;
         const int64_t nr = n0 + min(n + r, nv - 1);
         const float xs = p.x.s[nr];
+        // all of a row's gradients of h at once: one wait for memory instead of one a piece
+        uint2 dh[MODE == kGrads ? 4 * FW : 1];
+        if constexpr (MODE == kGrads) {
+            const uint16_t *src = p.dh + nr * M + m + 4 * h;
+            if (full) {
+#pragma unroll
+                for (int i = 0; i < 4 * FW; ++i)
+                    __builtin_memcpy(&dh[i], src + 8 * i, 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4 * FW; ++i)
+                    dh[i] = load4(src, 8 * i, M - (m + 8 * i + 4 * h));
+            }
+        }
         float4_t v[G], v2[MODE == kGrads ? G : 1];
 #pragma unroll
         for (int i = 0; i < FW; ++i) {
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4) {
-                const int64_t mr = m + 32 * i + 8 * v4 + 4 * h;
-                const float4_t ws = scales4(p.w.s, mr, M);
-                const float4_t g = scaled4(i, j, v4, ws, xs);
+                const float *row = sc + mw + 32 * i + 8 * v4 + 4 * h;
+                const float4_t g = scaled4(i, j, v4, *reinterpret_cast<const float4_t *>(row), xs);
                 if constexpr (MODE == kPlain) {
                     v[4 * i + v4] = g;
                 } else {
-                    const float4_t us = scales4(p.w2.s, mr, M);
-                    const float4_t u = scaled4(FW + i, j, v4, us, xs);
+                    const float4_t u = scaled4(FW + i, j, v4, *reinterpret_cast<const float4_t *>(row + BW), xs);
                     if constexpr (MODE == kGated) {
                         v[4 * i + v4] = float4_t{gated_value(g[0], u[0], p.act), gated_value(g[1], u[1], p.act),
                                                  gated_value(g[2], u[2], p.act), gated_value(g[3], u[3], p.act)};
                     } else {
-                        const float4_t d = load4(p.dh, nr * M + mr, M - mr, p.type);
+                        const float4_t fg = *reinterpret_cast<const float4_t *>(row + 2 * BW);
+                        const float4_t fu = *reinterpret_cast<const float4_t *>(row + 3 * BW);
+                        const float4_t d = values4(dh[4 * i + v4], p.type);
                         float4_t dg, du;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const Gate a = gate_grad(g[c], p.act);
-                            dg[c] = d[c] * u[c] * a.da * scale_fraction(ws[c]);
-                            du[c] = d[c] * a.a * scale_fraction(us[c]);
+                            dg[c] = d[c] * u[c] * a.da * fg[c];
+                            du[c] = d[c] * a.a * fu[c];
                         }
                         v[v4] = dg;
                         v2[v4] = du;
@@ -289,8 +317,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void i8_tile_kernel(I8TileArgs p)
 {
     constexpr int BM = 32 * FM * WM / (MODE == kPlain ? 1 : 2), BN = 32 * FN * WN;
     __shared__ __attribute__((aligned(16))) uint8_t lds[std::max(
-        i8_lds_bytes<WM, WN, FM, FN, NB>(),
-        cuts(FM) ? i8_lds_bytes<WM, WN, FM, FN / 2, NB + 1>() : 0)]; // (halves: one stage more)
+        i8_lds_bytes<MODE, WM, WN, FM, FN, NB>(),
+        cuts(FM) ? i8_lds_bytes<MODE, WM, WN, FM, FN / 2, NB + 1>() : 0)]; // (halves: one stage more)
     const TileWork work = tile_work(p.tiles_total, p.tiles_whole);
     if (work.tile < 0)
         return;
@@ -323,8 +351,12 @@ hipError_t launch_tiles(I8TileArgs p, hipStream_t st)
 }
 
 // The tile for a shape, from an estimate of the time of a stage (128 columns): full rounds of
-// tiles on the device, and a last one by how many CUs it has.
-int tile_choice(int64_t M, int64_t N)
+// tiles on the device, and a last one by how many CUs it has.  Measured, us for K 14336 (112
+// stages): 64 x 64 tiles 26 up to one per CU, 46 at two, 92 at four; 128 x 128 47 alone, 66 at
+// one per CU; 256 x 256 67 for a lone round in halves, 194 a full round.  So 4096 x 14336 takes by
+// 130 rows 26 us on the first (47, 67 on the others), by 1024 rows 66 on the second (93, 81), by
+// 4096 rows 194 on the third (356, 252).
+int tile_choice(int64_t M, int64_t N, bool pair)
 {
     const int64_t cus = device_cus();
     auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b); };
@@ -332,17 +364,21 @@ int tile_choice(int64_t M, int64_t N)
         return rest ? lone + (full - lone) * (double)rest / (double)cus : 0;
     };
     const int64_t t1 = tiles(64), t2 = tiles(128), t3 = tiles(256), whole = tiles_whole(t3, cus);
-    const double t64 = 0.39 + 0.36 * std::max(0.0, (double)t1 / (double)cus - 1.0);
-    const double t128 = 0.75 * (double)(t2 / cus) + last(t2 % cus, 0.63, 0.78);
-    const double t256 = 2.1 * (double)(t3 / cus) +
-                        (whole < t3 ? last(2 * (t3 - whole), 1.02, 1.22) : last(t3 % cus, 1.5, 2.1));
+    // (gate/up: the smallest tiles are 128 x 64; 14336 x 4096 by 64 rows 21 us, by 130 rows 44 on
+    // them and 37 on the largest)
+    const int64_t tp = (M + 127) / 128 * ((N + 63) / 64);
+    const double t64 = pair ? 0.5 + 0.39 * std::max(0.0, (double)tp / (double)cus - 1.0)
+                            : 0.22 + 0.195 * std::max(0.0, (double)t1 / (double)cus - 1.0);
+    const double t128 = 0.58 * (double)(t2 / cus) + last(t2 % cus, 0.42, 0.58);
+    const double t256 = 1.72 * (double)(t3 / cus) +
+                        (whole < t3 ? last(2 * (t3 - whole), 0.6, 1.15) : last(t3 % cus, 1.2, 1.72));
     return t64 <= t128 && t64 <= t256 ? 64 : t128 <= t256 ? 128 : 256;
 }
 
 template <int MODE>
 hipError_t launch_pair(const I8TileArgs &p, hipStream_t st)
 {
-    switch (tile_choice(2 * (int64_t)p.M, p.N)) {
+    switch (tile_choice(2 * (int64_t)p.M, p.N, true)) {
     case 64: return launch_tiles<MODE, 2, 2, 2, 1, 3>(p, st);
     case 128: return launch_tiles<MODE, 2, 2, 2, 2, 3>(p, st);
     default: return launch_tiles<MODE, 2, 4, 4, 2, 2>(p, st);
@@ -363,7 +399,7 @@ hipError_t launch_i8_tiles(I8Mat w, I8Mat x, void *y, int type, int64_t M, int64
     p.M = (int)M;
     p.K = (int)K;
     p.N = (int)N;
-    switch (tile_choice(M, N)) {
+    switch (tile_choice(M, N, false)) {
     case 64: return launch_tiles<kPlain, 2, 2, 1, 1, 4>(p, st);
     case 128: return launch_tiles<kPlain, 2, 2, 2, 2, 3>(p, st);
     default: return launch_tiles<kPlain, 2, 4, 4, 2, 2>(p, st);

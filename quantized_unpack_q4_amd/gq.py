@@ -852,11 +852,6 @@ def _i8_matrix(name, q, s, dev):
     return qa, ld, _mx_addr(name + " scales", s, dev, _torch.float32, (rows,)), rows, K
 
 
-def _i8_new(rows, K, like, stream):
-    """New codes [rows][K], rows a multiple of 16 bytes apart."""
-    return _mx_new((rows, (K + 15) & -16), _torch.int8, like, stream)[:, :K]
-
-
 def _i8_pair(gate, up, dev):
     ga, gld, gs, I, H = _i8_matrix("w_gate", *gate, dev)
     ua, uld, us, I2, H2 = _i8_matrix("w_up", *up, dev)
@@ -893,12 +888,16 @@ def quantize_i8(x, out=None, stream=None):
     code = _mx_dtype(x.dtype)
     N, K, ldx = _rows_2d("x", x)
     if out is None:
-        q, s = _i8_new(N, K, x, stream), _mx_new((N,), torch.float32, x, stream)
+        ldq = (K + 15) & -16
+        q, s = _mx_new((N, ldq), torch.int8, x, stream), _mx_new((N,), torch.float32, x, stream)
+        qa, sa = q.data_ptr(), s.data_ptr()
+        if ldq != K:
+            q = q[:, :K]
     else:
         q, s = out
-    qa, ldq, sa, rows, KQ = _i8_matrix("codes", q, s, dev)
-    if (rows, KQ) != (N, K):
-        raise ValueError("codes have shape (%d, %d), expected (%d, %d)" % (rows, KQ, N, K))
+        qa, ldq, sa, rows, KQ = _i8_matrix("codes", q, s, dev)
+        if (rows, KQ) != (N, K):
+            raise ValueError("codes have shape (%d, %d), expected (%d, %d)" % (rows, KQ, N, K))
     _check(lib().gq_quantize_i8(x.data_ptr(), code, ldx, qa, ldq, sa, N, K,
                                 _mx_stream(stream, dev)))
     return q, s
