@@ -49,19 +49,6 @@ __device__ __forceinline__ float16_t mfma32_16(uint4 a, uint4 b, float16_t c)
                                                       __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
 }
 
-// Weights of byte `c` of eight rows' dwords as packed 16-bit values: q s rounded to binary32 and
-// then to the type.
-template <bool BF16, int c>
-__device__ __forceinline__ uint4 weights8(const uint32_t (&w)[8], const float (&s)[8])
-{
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = as_is((float)(int8_t)(w[i] >> (8 * c)) * s[i]);
-    return make_uint4(mx_pack2<BF16>(v[0], v[1]), mx_pack2<BF16>(v[2], v[3]),
-                      mx_pack2<BF16>(v[4], v[5]), mx_pack2<BF16>(v[6], v[7]));
-}
-
 template <bool BF16, bool SPLIT, int WM, int WN, int FN, bool TAIL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
 {
@@ -98,73 +85,95 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         dchk[i] = (lane & 7) ^ swz8(row);
     }
     const uint32_t base = lds_addr(lds);
-    // stage t of the run: stage st of part pt (past the last: the last again)
-    auto where = [&](int t, int &pt, int &st) {
-        t = first + min(t, total - 1);
-        pt = t >= nst ? 1 : 0;
-        st = t - pt * nst;
+    // d, stage after stage of the run (past the last: the last again)
+    int dst = first >= nst ? first - nst : first, dleft = total;
+    const uint16_t *dq = (first >= nst ? p.part[1].d + 0 : p.part[0].d + 0) + (int64_t)n0 * p.ldd +
+                         (int64_t)dst * 64;
+    auto copy_d = [&](int b, int i) {
+        const uint32_t last = (uint32_t)(nch - 1 - 8 * dst); // chunks past it repeat it
+        load_lds16(dq, doff[i] + 16u * (TAIL ? min(dchk[i], last) : dchk[i]),
+                   __builtin_amdgcn_readfirstlane(base + kD + b * (BN * 128) + 1024u * (CX * wave + i)));
     };
-    auto copy_d = [&](int t, int i) {
-        int pt, st;
-        where(t, pt, st);
-        const uint16_t *d = pt ? p.part[1].d : p.part[0].d;
-        const uint32_t last = (uint32_t)(nch - 1 - 8 * st); // chunks past it repeat it
-        load_lds16(d + (int64_t)n0 * p.ldd + (int64_t)st * 64, doff[i] + 16u * (TAIL ? min(dchk[i], last) : dchk[i]),
-                   __builtin_amdgcn_readfirstlane(base + kD + (t & 1) * (BN * 128) +
-                                                  1024u * (CX * wave + i)));
+    auto next_d = [&] {
+        if (--dleft <= 0)
+            return;
+        dq += 64;
+        if (++dst == nst) {
+            dst = 0;
+            dq = p.part[1].d + (int64_t)n0 * p.ldd;
+        }
     };
     // weights: unit u of this thread, rows 8 c .. 8 c + 7 of columns 4 l .. 4 l + 3
     struct Raw {
         uint32_t w[8];
         float s[8];
     };
-    const int lastcol = ((K + 15) & ~15) - 4;
     int urow[UN], ucol[UN], uput[UN][4];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
         const int id = tid + NT * u, c = id / (BK / 4), l = id % (BK / 4);
         urow[u] = 8 * c;
-        ucol[u] = min(k0 + 4 * l, lastcol);
+        ucol[u] = min(k0 + 4 * l, ((K + 15) & ~15) - 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = (BK / 4) * i + l;
             uput[u][i] = row * 128 + 16 * (c ^ swz8(row));
         }
     }
-    auto load_w = [&](int t, Raw (&raw)[UN]) {
-        int pt, st;
-        where(t, pt, st);
-        const int8_t *q = pt ? p.part[1].w.q + 0 : p.part[0].w.q + 0;
-        const float *s = (pt ? p.part[1].w.s + 0 : p.part[0].w.s + 0) + 64 * (int64_t)st;
-        const uint32_t ld = (uint32_t)(pt ? p.part[1].w.ld + 0 : p.part[0].w.ld + 0);
-        q += 64 * (int64_t)st * ld;
-        const int left = M - 64 * st; // rows past it repeat the last
+    int wst, wleft = total;
+    const int8_t *wq;
+    const float *wsc;
+    uint32_t ld, uoff[UN][8];
+    auto enter = [&](const I8Mat &w, int st) { // stage st of a matrix
+        wst = st;
+        ld = (uint32_t)w.ld;
+        wq = w.q + 64 * (int64_t)st * ld;
+        wsc = w.s + 64 * (int64_t)st;
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                uoff[u][i] = (uint32_t)(urow[u] + i) * ld + (uint32_t)ucol[u];
+    };
+    if (first >= nst)
+        enter(p.part[1].w, first - nst);
+    else
+        enter(p.part[0].w, first);
+    auto load_w = [&](Raw (&raw)[UN]) {
+        const int left = M - 64 * wst; // rows past it repeat the last
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             if (!TAIL || left >= 64) {
-                const uint32_t off = (uint32_t)urow[u] * ld + (uint32_t)ucol[u];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    raw[u].w[i] = load_dword(q + (uint64_t)i * ld, off);
-                *reinterpret_cast<float4 *>(raw[u].s) = ldf4(s + urow[u]);
-                *reinterpret_cast<float4 *>(raw[u].s + 4) = ldf4(s + urow[u] + 4);
+                    raw[u].w[i] = load_dword(wq, uoff[u][i]);
+                *reinterpret_cast<float4 *>(raw[u].s) = ldf4(wsc + urow[u]);
+                *reinterpret_cast<float4 *>(raw[u].s + 4) = ldf4(wsc + urow[u] + 4);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int m = min(urow[u] + i, left - 1);
-                    raw[u].w[i] = load_dword(q, (uint32_t)m * ld + (uint32_t)ucol[u]);
-                    raw[u].s[i] = s[m];
+                    raw[u].w[i] = load_dword(wq, (uint32_t)m * ld + (uint32_t)ucol[u]);
+                    raw[u].s[i] = wsc[m];
                 }
             }
         }
+        if (--wleft <= 0) // (past the last stage: the last again)
+            return;
+        wq += 64 * (int64_t)ld;
+        wsc += 64;
+        if (++wst == nst)
+            enter(p.part[1].w, 0);
     };
-    // once loaded: a tile of 256 columns has one unit's rows in all lanes of a wave, their scales
-    // then go to scalar registers
+    // Once loaded (the compiler waits here, where nothing else is in flight): a tile of 256
+    // columns has one unit's rows in all lanes of a wave, their scales then go to scalar
+    // registers.
     auto ready = [&](Raw (&raw)[UN]) {
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                asm volatile("" : "+v"(raw[u].w[i]), "+v"(raw[u].s[i]));
                 if constexpr (BK == 256)
                     raw[u].s[i] = __builtin_bit_cast(
                         float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, raw[u].s[i])));
@@ -172,13 +181,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
                     raw[u].s[i] = scale_pow2(raw[u].s[i]);
             }
     };
-    // column i of the units: 16 bytes each into buffer b
-    auto put_w = [&](const Raw (&raw)[UN], auto ic, int b) {
+    // Column i of the units into buffer b, in NM pieces, one after each product of a step: q s of
+    // a piece's rows, rounded to binary32 and then to the type; a unit's eight are 16 bytes.
+    constexpr int NM = 4 * FN, PW = 8 * UN / NM;
+    static_assert(PW * NM == 8 * UN, "whole pieces");
+    float pv = 0;
+    uint32_t pk[4];
+    auto put_w = [&](const Raw (&raw)[UN], auto ic, int b, int piece) {
         constexpr int i = decltype(ic)::value;
 #pragma unroll
-        for (int u = 0; u < UN; ++u)
-            *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + uput[u][i]) =
-                weights8<BF16, i>(raw[u].w, raw[u].s);
+        for (int e = piece * PW; e < piece * PW + PW; ++e) {
+            const int u = e / 8, j = e % 8;
+            const float v = as_is((float)(int8_t)(raw[u].w[j] >> (8 * i)) * raw[u].s[j]);
+            if (j % 2)
+                pk[j / 2] = mx_pack2<BF16>(pv, v);
+            else
+                pv = v;
+            if (j == 7)
+                *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + uput[u][i]) =
+                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
     };
 
     float16_t acc[4][FN];
@@ -205,7 +227,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
             f.b[j] = ld16(D + 32 * j * 128);
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto multiply = [&](int t, int s, Frag &f) {
+    // the products of a step; between(u) after each of them, in the shadow of the matrix
+    // instruction
+    auto multiply = [&](int t, int s, Frag &f, auto between) {
         if constexpr (TAIL) { // gradients past M are zero (they may be anything)
             const int st = first + t >= nst ? first + t - nst : first + t;
             const bool none = 8 * st + 2 * s + h >= nch;
@@ -223,6 +247,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
             for (int j = 0; j < FN; ++j) {
                 acc[i][j] = mfma32_16<BF16>(f.a[i], f.b[j], acc[i][j]);
                 asm volatile("" : "+v"(acc[i][j]));
+                between(i * FN + j);
+                __builtin_amdgcn_sched_barrier(0);
             }
     };
     using I0 = std::integral_constant<int, 0>;
@@ -231,43 +257,50 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     using I3 = std::integral_constant<int, 3>;
 
     // Stage t: the products of its buffers; its waves put the weights of stage t + 1, loaded
-    // a stage ago, into the other buffers, and start the loads of stage t + 2 and the copies of
-    // d of stage t + 1.  (The compiler does not know that `put` has landed: its wait for that
-    // comes before anything else is in flight.)
+    // a stage ago, into the other buffers, and start the copies of d of stage t + 1 and the loads
+    // of stage t + 2.
     Frag f0, f1;
-    auto stage = [&](int t, Raw (&put)[UN], Raw (&load)[UN]) {
-        read(t, 1, f1);
-        ready(put);
-        put_w(put, I0{}, (t + 1) & 1);
+    auto stage = [&](int t, const Raw (&put)[UN], Raw (&load)[UN]) {
+        const int b = (t + 1) & 1;
 #pragma unroll
         for (int i = 0; i < CX; ++i)
-            copy_d(t + 1, i);
-        load_w(t + 2, load);
-        multiply(t, 0, f0);
+            copy_d(b, i);
+        next_d();
+        read(t, 1, f1);
+        multiply(t, 0, f0, [&](int u) { put_w(put, I0{}, b, u); });
+        load_w(load);
         read(t, 2, f0);
-        put_w(put, I1{}, (t + 1) & 1);
-        multiply(t, 1, f1);
+        multiply(t, 1, f1, [&](int u) { put_w(put, I1{}, b, u); });
         read(t, 3, f1);
-        put_w(put, I2{}, (t + 1) & 1);
-        multiply(t, 2, f0);
-        put_w(put, I3{}, (t + 1) & 1);
-        multiply(t, 3, f1);
+        multiply(t, 2, f0, [&](int u) { put_w(put, I2{}, b, u); });
+        multiply(t, 3, f1, [&](int u) { put_w(put, I3{}, b, u); });
         // the next stage is converted and copied, and every wave has read this one
         wait_copies<0>();
+        ready(load);
         read(t + 1, 0, f0); // (after the last stage: read and not used)
     };
     Raw r0[UN], r1[UN];
-    load_w(0, r0);
+    load_w(r0);
+    load_w(r1);
     ready(r0);
-    put_w(r0, I0{}, 0);
-    put_w(r0, I1{}, 0);
-    put_w(r0, I2{}, 0);
-    put_w(r0, I3{}, 0);
-    load_w(1, r1);
+#pragma unroll
+    for (int u = 0; u < NM; ++u)
+        put_w(r0, I0{}, 0, u);
+#pragma unroll
+    for (int u = 0; u < NM; ++u)
+        put_w(r0, I1{}, 0, u);
+#pragma unroll
+    for (int u = 0; u < NM; ++u)
+        put_w(r0, I2{}, 0, u);
+#pragma unroll
+    for (int u = 0; u < NM; ++u)
+        put_w(r0, I3{}, 0, u);
 #pragma unroll
     for (int i = 0; i < CX; ++i)
         copy_d(0, i);
+    next_d();
     wait_copies<0>();
+    ready(r1);
     read(0, 0, f0);
     for (int t = 0; t < total; t += 2) {
         stage(t, r1, r0);
