@@ -185,8 +185,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     // a piece's rows, rounded to binary32 and then to the type; a unit's eight are 16 bytes.
     constexpr int NM = 4 * FN, PW = 8 * UN / NM;
     static_assert(PW * NM == 8 * UN, "whole pieces");
-    float pv = 0;
-    uint32_t pk[4];
+    float pv[4];
+    uint32_t pk[4][4];
     auto put_w = [&](const Raw (&raw)[UN], auto ic, int b, int piece) {
         constexpr int i = decltype(ic)::value;
 #pragma unroll
@@ -194,12 +194,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
             const int u = e / 8, j = e % 8;
             const float v = as_is((float)(int8_t)(raw[u].w[j] >> (8 * i)) * raw[u].s[j]);
             if (j % 2)
-                pk[j / 2] = mx_pack2<BF16>(pv, v);
+                pk[i][j / 2] = mx_pack2<BF16>(pv[i], v);
             else
-                pv = v;
+                pv[i] = v;
             if (j == 7)
                 *reinterpret_cast<uint4 *>(lds + b * (BK * 128) + uput[u][i]) =
-                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    make_uint4(pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
         }
     };
 
@@ -266,18 +266,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         for (int i = 0; i < CX; ++i)
             copy_d(b, i);
         next_d();
+        load_w(load);
         read(t, 1, f1);
         multiply(t, 0, f0, [&](int u) { put_w(put, I0{}, b, u); });
-        load_w(load);
         read(t, 2, f0);
-        multiply(t, 1, f1, [&](int u) { put_w(put, I1{}, b, u); });
+        multiply(t, 1, f1, [&](int u) {
+            put_w(put, I1{}, b, u);
+            put_w(put, I2{}, b, u);
+        });
         read(t, 3, f1);
-        multiply(t, 2, f0, [&](int u) { put_w(put, I2{}, b, u); });
-        multiply(t, 3, f1, [&](int u) { put_w(put, I3{}, b, u); });
-        // the next stage is converted and copied, and every wave has read this one
+        multiply(t, 2, f0, [&](int u) { put_w(put, I3{}, b, u); });
+        // the next stage is converted and copied, and every wave has read this one; its last
+        // products run while the next one's first operands are read
         wait_copies<0>();
-        ready(load);
         read(t + 1, 0, f0); // (after the last stage: read and not used)
+        multiply(t, 3, f1, [](int) {});
+        ready(load);
     };
     Raw r0[UN], r1[UN];
     load_w(r0);
