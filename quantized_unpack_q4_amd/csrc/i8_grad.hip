@@ -314,7 +314,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     wait_copies<0>();
 
     // element v of accumulator i: column 4 (8 (v / 4) + 4 h + v % 4) + i, row r
-    const bool vec = K % 8 == 0; // rows start 16-byte aligned
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const int n = 32 * (FN * wn + j) + r;
@@ -344,9 +343,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
                 o[2 * c] = mx_pack2<BF16>(acc[0][j][4 * g + c], acc[1][j][4 * g + c]);
                 o[2 * c + 1] = mx_pack2<BF16>(acc[2][j][4 * g + c], acc[3][j][4 * g + c]);
             }
-            if (vec && k + 16 <= K) {
-                *reinterpret_cast<uint4 *>(out + k) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(out + k + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            if (k + 16 <= K) { // (rows need not start 16-byte aligned)
+                __builtin_memcpy(out + k, o, 32);
             } else {
 #pragma unroll
                 for (int c = 0; c < 16; ++c)

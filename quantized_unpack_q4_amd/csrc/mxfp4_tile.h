@@ -90,7 +90,6 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
                                                        mx_pack2<TYPE == kBF16>(v[g][2], v[g][3]));
     }
     lds_wave_order();
-    const bool vec = ld % CE == 0; // rows start 16-byte aligned
     const int64_t mleft = M - m;
 #pragma unroll
     for (int k = 0; k < 32 * CPR / 64; ++k) {
@@ -99,8 +98,9 @@ __device__ __forceinline__ void store_rows(uint8_t *scr, void *y, int64_t n, int
             continue;
         const uint8_t *s = scr + row * ST + col * ES;
         uint8_t *d = reinterpret_cast<uint8_t *>(y) + ((n + row) * ld + m + col) * ES;
-        if (vec && col + CE <= mleft) {
-            *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(s);
+        if (col + CE <= mleft) { // (rows need not start 16-byte aligned)
+            const uint4 c = *reinterpret_cast<const uint4 *>(s);
+            __builtin_memcpy(d, &c, 16);
         } else {
 #pragma unroll
             for (int i = 0; i < CE; ++i)
