@@ -43,8 +43,12 @@ constexpr int codes_bytes(int W, int B, int run) { return W * B * (run + 16); }
 template <int SRC, bool PAIR, int W, int LDSB>
 __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 {
-    constexpr int P = PAIR ? 2 : 1, U = 8; // U steps loaded at once
     constexpr bool FLOATS = SRC != kCodes;
+    constexpr int P = PAIR ? 2 : 1;
+    // Steps loaded at once.  With the next tile's on their way while a tile is joined, few are
+    // enough, and the registers go to more waves: gate and up of 14336 x 4096 by one row, from
+    // HBM, 24.3 us (4.8 TB/s) with two, 25.3 with four, 30 with eight.
+    constexpr int U = FLOATS && PAIR ? 2 : 4;
     __shared__ __attribute__((aligned(16))) uint8_t codes[FLOATS ? LDSB : 16];
     __shared__ uint32_t part[4][W];
     __shared__ float xscale[4];
@@ -123,6 +127,8 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
                 *reinterpret_cast<uint2 *>(mine + b * pitch + c) = i8_codes8(x[i], rb);
         }
         lds_wave_order();
+    } else {
+        load(blockIdx.x, 0, now);
     }
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -132,7 +138,7 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
         for (int i = 0; i < P; ++i)
             acc[i] = int4v{0, 0, 0, 0};
         for (int s0 = 0; s0 < steps; s0 += U) {
-            if (s0 > 0 || !FLOATS)
+            if (s0 > 0)
                 load(tile, s0, now);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
                     acc[i] = mfma16_i8(now.a[i][u], xv, acc[i]);
             }
         }
-        if (FLOATS && tile + (int)gridDim.x < tiles) // while this tile's sums are joined
+        if (tile + (int)gridDim.x < tiles) // while this tile's sums are joined
             load(tile + gridDim.x, 0, now);
 #pragma unroll
         for (int i = 0; i < P; ++i)
@@ -207,11 +213,12 @@ template <int SRC, bool PAIR>
 hipError_t launch_stream(const I8StreamArgs &p, hipStream_t st)
 {
     const int64_t tiles = ((int64_t)p.M + 15) / 16;
-    // Floats: as many workgroups as the CUs hold at once, which quantise once for all of their
-    // tiles (14336 x 4096, batch 4: 17 us, with a workgroup a tile 24).  Codes: one a tile.
-    const int64_t most = SRC == kCodes ? tiles : (p.K > kLongK ? 1 : 2) * device_cus();
-    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, std::min(tiles, most), st)
-                        : launch_waves<SRC, PAIR, 8>(p, std::min(tiles, most), st);
+    // As many workgroups as the CUs hold at once, which quantise once for all of their tiles
+    // (14336 x 4096, batch 4: 17 us, with a workgroup a tile 24), equally many each (gate and up
+    // of 14336 rows, 896 tiles, on 448 workgroups instead of 512: 27.6 us, 30.3).
+    const int64_t most = (p.K > kLongK ? 1 : 2) * device_cus(), each = (tiles + most - 1) / most;
+    const int64_t grid = (tiles + each - 1) / each;
+    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, grid, st) : launch_waves<SRC, PAIR, 8>(p, grid, st);
 }
 
 template <bool PAIR>
