@@ -230,15 +230,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     // the products of a step; between(u) after each of them, in the shadow of the matrix
     // instruction
     auto multiply = [&](int t, int s, Frag &f, auto between) {
-        if constexpr (TAIL) { // gradients past M are zero (they may be anything)
+        if constexpr (TAIL) {
             const int st = first + t >= nst ? first + t - nst : first + t;
-            const bool none = 8 * st + 2 * s + h >= nch;
+            if (st == nst - 1) { // gradients past M are zero (they may be anything)
+                asm volatile(""); // (a branch, not a selection in every stage)
+                const bool none = 8 * st + 2 * s + h >= nch;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                f.b[j].x = none ? 0 : f.b[j].x;
-                f.b[j].y = none ? 0 : f.b[j].y;
-                f.b[j].z = none ? 0 : f.b[j].z;
-                f.b[j].w = none ? 0 : f.b[j].w;
+                for (int j = 0; j < FN; ++j) {
+                    f.b[j].x = none ? 0 : f.b[j].x;
+                    f.b[j].y = none ? 0 : f.b[j].y;
+                    f.b[j].z = none ? 0 : f.b[j].z;
+                    f.b[j].w = none ? 0 : f.b[j].w;
+                }
             }
         }
 #pragma unroll
