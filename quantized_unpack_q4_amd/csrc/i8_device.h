@@ -51,15 +51,6 @@ struct I8Row {
     __device__ __forceinline__ I8Row(float top_, float s_, float r_) : top(top_), s(s_), r(r_) {}
 };
 
-template <int TYPE>
-__device__ __forceinline__ float i8_load(const void *x, int64_t i)
-{
-    if constexpr (TYPE == kF32)
-        return reinterpret_cast<const float *>(x)[i];
-    const uint32_t u = reinterpret_cast<const uint16_t *>(x)[i];
-    return TYPE == kBF16 ? __builtin_bit_cast(float, u << 16) : half_to_float(u);
-}
-
 // A binary32 value as it stands: without this the compiler may merge its last operation and the
 // rounding to binary16 into one instruction with one rounding, and results would depend on
 // which kernel, and which type, they were formed in.

@@ -14,6 +14,19 @@
 // time go to consecutive rows (distinct banks), and a wave's four fragments, i = 0 .. 3 of the
 // same l, hold 128 consecutive columns, sixteen of them consecutive in a lane's accumulators,
 // which are stored as they lie.
+//
+// Where tiles are too few to fill the device the sum is cut into runs, a workgroup each, whose
+// binary32 sums a second launch adds in run order.
+//
+// What bounds it on 256 x 256 tiles: 4096 x 14336 by 2048 rows takes 233 us (1.03 PFLOP/s; the
+// library's bfloat16 products of 16384 x 16384 matrices reach 1.60), 4096 x 4096 by 4096 rows, one
+// full round, 118 (1.16).  Of those 118, products, operand reads and barriers alone take 93; copies
+// and loads add 11, conversions and their stores 12.  Steps that got there: conversions from
+// unsigned bytes with a fused step and per-stage selections of what becomes of a scale 172 us,
+// signed ones (two instructions a weight), scales in scalar registers, masks in the last stage
+// only 124; conversions between the products and the last products after the barrier 118.
+// Tried and not kept: 128 x 128 per wave on four waves (spills), weights loaded two stages ahead
+// (130 us: registers).
 #include <algorithm>
 #include <type_traits>
 
@@ -419,6 +432,12 @@ constexpr GradTile kTiles[] = {{256, 256, 1, 1.7}, {256, 128, 1, 1.2}, {128, 64,
 struct GradPlan {
     int tile, splits;
 };
+// The tile and the number of runs with the least estimated time: rounds of workgroups on the
+// device's 256 CUs, 4 us for a workgroup's start and end; runs add a launch and the traffic of
+// their sums.  Measured, us (tiles of 256 x 256, 256 x 128, 128 x 64, with the best number of runs):
+// 4096 x 4096 by 16 rows 17 (16 runs), 15 (16), 15 (8); by 130 rows 31 (16), 28 (8), 27 (8), in one
+// run 93, 65, 58; by 512 rows 48 (4), 40 (4), 51 (4); 14336 x 4096 by 2048 rows 228 (2), 248 (1),
+// 402 (4).
 GradPlan grad_plan(int nparts, int64_t M, int64_t K, int64_t N)
 {
     constexpr int64_t kCus = 256;

@@ -1,6 +1,11 @@
 // i8_stream.hip -- int8 products by up to 16 activation rows, weights streamed once.
 //
-// A workgroup takes tiles of 16 weight rows (of each matrix in the gate/up form); its W waves
+// What bounds them is the weight stream: from HBM, 14336 x 4096 takes 14.3 us by one bfloat16 row
+// (4.1 TB/s), gate and up of that size 24.5 (4.8 TB/s; a large copy 5.1), 4096 x 14336 14.4; by 16
+// rows of codes 18.1 and 18.6.  Matrices of 4096 x 4096 and less take 7 us, most of it start, one
+// latency of memory and the join.
+//
+// A workgroup takes tiles of 16 or 32 weight rows (of each matrix in the gate/up form); its W waves
 // share K, a contiguous run each, and multiply on the 16x16x64 product, whose operand is 16
 // codes (16 bytes) of a row per lane as they lie in memory.  The waves' sums are whole numbers:
 // joined through LDS they are the same in any order.
@@ -40,19 +45,19 @@ __device__ __forceinline__ int4v mfma16_i8(uint4 a, uint4 b, int4v c)
 // that 16 rows' reads touch distinct banks.
 constexpr int codes_bytes(int W, int B, int run) { return W * B * (run + 16); }
 
-template <int SRC, bool PAIR, int W, int LDSB>
+template <int SRC, bool PAIR, int W, int R, int LDSB>
 __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 {
     constexpr bool FLOATS = SRC != kCodes;
-    constexpr int P = PAIR ? 2 : 1;
+    constexpr int P = PAIR ? 2 : 1, TR = 16 * R; // matrices, weight rows of a tile
     // Steps loaded at once.  With the next tile's on their way while a tile is joined, few are
     // enough, and the registers go to more waves: gate and up of 14336 x 4096 by one row, from
-    // HBM, 24.3 us (4.8 TB/s) with two, 25.3 with four, 30 with eight.
-    constexpr int U = FLOATS && PAIR ? 2 : 4;
+    // HBM, 24.3 us with two, 25.3 with four, 30 with eight.
+    constexpr int U = PAIR ? 2 : 4;
     __shared__ __attribute__((aligned(16))) uint8_t codes[FLOATS ? LDSB : 16];
     __shared__ uint32_t part[4][W];
     __shared__ float xscale[4];
-    __shared__ int4v red[W][P][64];
+    __shared__ int4v red[W][P][R][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
@@ -63,16 +68,22 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
     const int pitch = p.run + 16;
     uint8_t *mine = codes + (FLOATS ? wave * B * pitch : 0);
 
-    const int tiles = (M + 15) >> 4;
+    const int tiles = (M + TR - 1) / TR;
     const int xr = min(r, B - 1);
     const int8_t *xp = FLOATS ? nullptr : p.xc.q + xr * p.xc.ld;
     // weights (and codes of activations) of U steps from s0
     struct Batch {
-        uint4 a[P][U], x[FLOATS ? 1 : U];
+        uint4 a[P][R][U], x[FLOATS ? 1 : U];
     };
     auto load = [&](int tile, int s0, Batch &t) {
-        const int64_t wr = min(16 * tile + r, M - 1);
-        const int8_t *wp[2] = {p.w.q + wr * p.w.ld, PAIR ? p.w2.q + wr * p.w2.ld : nullptr};
+        const int8_t *wp[P][R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int64_t wr = min(TR * tile + 16 * j + r, M - 1);
+            wp[0][j] = p.w.q + wr * p.w.ld;
+            if constexpr (PAIR)
+                wp[P - 1][j] = p.w2.q + wr * p.w2.ld;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u >= steps)
@@ -80,7 +91,9 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
             const int ch = min((k0 >> 4) + 4 * (s0 + u) + q, lastc);
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                t.a[i][u] = ld16(wp[i] + 16 * ch);
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    t.a[i][j][u] = ld16(wp[i][j] + 16 * ch);
             if constexpr (!FLOATS)
                 t.x[u] = ld16(xp + 16 * ch);
         }
@@ -132,11 +145,13 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
     }
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int m0 = 16 * tile;
-        int4v acc[P];
+        const int m0 = TR * tile;
+        int4v acc[P][R];
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            acc[i] = int4v{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                acc[i][j] = int4v{0, 0, 0, 0};
         for (int s0 = 0; s0 < steps; s0 += U) {
             if (s0 > 0)
                 load(tile, s0, now);
@@ -162,32 +177,38 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
                 }
 #pragma unroll
                 for (int i = 0; i < P; ++i)
-                    acc[i] = mfma16_i8(now.a[i][u], xv, acc[i]);
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        acc[i][j] = mfma16_i8(now.a[i][j][u], xv, acc[i][j]);
             }
         }
         if (tile + (int)gridDim.x < tiles) // while this tile's sums are joined
             load(tile + gridDim.x, 0, now);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            red[wave][i][lane] = acc[i];
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                red[wave][i][j][lane] = acc[i][j];
         __syncthreads();
-        // output t: weight row t % 16, activation row t / 16; in the accumulators lane
-        // 16 (row / 4) + activation row, element row % 4
-        if (tid < 256 && tid >> 4 < B && m0 + (tid & 15) < M) {
-            const int m = tid & 15, b = tid >> 4, from = 16 * (m >> 2) + b;
+        // output t: weight row t % 16 of group t / 256, activation row t / 16 % 16; in the
+        // accumulators lane 16 (row / 4) + activation row, element row % 4
+        const int m = tid & 15, b = tid >> 4 & 15, g = tid >> 8, from = 16 * (m >> 2) + b;
+        const int row = m0 + 16 * g + m;
+        static_assert(W * 64 >= 256 * R, "a thread for every output");
+        if (g < R && b < B && row < M) {
             int sum[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 sum[i] = 0;
 #pragma unroll
                 for (int j = 0; j < W; ++j)
-                    sum[i] += red[j][i][from][m & 3];
+                    sum[i] += red[j][i][g][from][m & 3];
             }
             const float xs = FLOATS ? xscale[b] : p.xc.s[b];
-            float v = i8_scaled(sum[0], p.w.s[m0 + m], xs);
+            float v = i8_scaled(sum[0], p.w.s[row], xs);
             if constexpr (PAIR)
-                v = gated_value(v, i8_scaled(sum[P - 1], p.w2.s[m0 + m], xs), p.act);
-            i8_store(p.y, (int64_t)b * M + m0 + m, p.type, v);
+                v = gated_value(v, i8_scaled(sum[P - 1], p.w2.s[row], xs), p.act);
+            i8_store(p.y, (int64_t)b * M + row, p.type, v);
         }
         __syncthreads();
     }
@@ -196,15 +217,21 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
 // Sixteen waves where K is long enough to keep eight waiting for their weights.
 constexpr int64_t kLongK = 8192;
 
-template <int SRC, bool PAIR, int W>
-hipError_t launch_waves(I8StreamArgs p, int64_t grid, hipStream_t st)
+template <int SRC, bool PAIR, int W, int R>
+hipError_t launch_waves(I8StreamArgs p, hipStream_t st)
 {
     // codes of up to four rows: see i8_fused
     constexpr int LDSB = SRC == kCodes ? 16 : std::max(codes_bytes(W, 4, 512), codes_bytes(W, 1, 1024));
     p.run = ((p.K + W - 1) / W + 63) / 64 * 64;
     if (SRC != kCodes && (!i8_fused(p.K, p.B) || codes_bytes(W, p.B, p.run) > LDSB))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, LDSB>), dim3((unsigned)grid), dim3(64 * W), 0, st,
+    // As many workgroups as the CUs hold at once, which quantise once for all of their tiles
+    // (14336 x 4096, batch 4: 17 us, with a workgroup a tile 24), equally many each (gate and up
+    // of 14336 rows, 896 tiles, on 448 workgroups instead of 512: 27.6 us, 30.3).
+    const int64_t tiles = ((int64_t)p.M + 16 * R - 1) / (16 * R);
+    const int64_t most = (W == 8 ? 2 : 1) * device_cus(), each = (tiles + most - 1) / most;
+    const int64_t grid = (tiles + each - 1) / each;
+    hipLaunchKernelGGL((i8_stream_kernel<SRC, PAIR, W, R, LDSB>), dim3((unsigned)grid), dim3(64 * W), 0, st,
                        p);
     return hipGetLastError();
 }
@@ -212,13 +239,12 @@ hipError_t launch_waves(I8StreamArgs p, int64_t grid, hipStream_t st)
 template <int SRC, bool PAIR>
 hipError_t launch_stream(const I8StreamArgs &p, hipStream_t st)
 {
-    const int64_t tiles = ((int64_t)p.M + 15) / 16;
-    // As many workgroups as the CUs hold at once, which quantise once for all of their tiles
-    // (14336 x 4096, batch 4: 17 us, with a workgroup a tile 24), equally many each (gate and up
-    // of 14336 rows, 896 tiles, on 448 workgroups instead of 512: 27.6 us, 30.3).
-    const int64_t most = (p.K > kLongK ? 1 : 2) * device_cus(), each = (tiles + most - 1) / most;
-    const int64_t grid = (tiles + each - 1) / each;
-    return p.K > kLongK ? launch_waves<SRC, PAIR, 16>(p, grid, st) : launch_waves<SRC, PAIR, 8>(p, grid, st);
+    // Codes of activations are read once a tile: tiles of 32 rows where they fill the device
+    // (14336 x 4096 by 16 rows 20.7 -> 18.1 us).
+    if constexpr (SRC == kCodes)
+        if (p.M >= 32 * device_cus())
+            return p.K > kLongK ? launch_waves<SRC, PAIR, 16, 2>(p, st) : launch_waves<SRC, PAIR, 8, 2>(p, st);
+    return p.K > kLongK ? launch_waves<SRC, PAIR, 16, 1>(p, st) : launch_waves<SRC, PAIR, 8, 1>(p, st);
 }
 
 template <bool PAIR>

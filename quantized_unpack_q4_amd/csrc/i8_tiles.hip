@@ -6,9 +6,17 @@
 // by direct copies, 128 columns (128 bytes of a row: whole cache lines) per stage, NB stages in
 // turn; operands are read a step ahead of the products, copies are issued between them.
 //
+// What bounds it, on 256 x 256 tiles: the matrix cores under the power limit.  4096 x 14336 by 4096
+// rows takes 190 us (2.5 POP/s; the library's product of 16384 x 16384 matrices 2.4), and the same
+// products on unchanging registers, without copies and LDS reads, 150 to 180 (by the codes'
+// values).  14336 x 4096 by 4096
+// rows, 3.5 rounds of tiles, takes 208 (200 with the weights in a cache).  64 x 64 tiles are bound
+// by what a CU reads from the L2 (4096 x 14336 by 130 rows 33 us from HBM, 26 again), two groups of
+// waves with a run of K each took as long.  128 x 128 per wave (four waves) was 4% slower.
+//
 // Gate/up: half of a tile's weight rows are rows of the gate matrix, half the same rows of the
 // up matrix, and a wave holds both of a row: h, or the gradients of g and u, is formed in
-// registers.
+// registers: 14336 x 4096 by 1024 rows takes 116 us, with the gradients of g and u 128.
 //
 // The last stage of a K that is no multiple of 128: copies past a row's last 16 bytes repeat
 // those, and the weights' codes past K are zeroed in registers (what lies there in the

@@ -32,6 +32,22 @@ def test_product_tiles(M, K, N, t):
          i8.round_to(i8.product(wq, ws, xq, xs), t), "gemm")
 
 
+@pytest.mark.parametrize("M,K,N", [(8192, 200, 16), (8207, 1000, 5), (9000, 8200, 3), (8191, 8192, 2),
+                                   (8300, 9001, 16)])
+def test_streamed_products_of_tall_matrices(M, K, N):
+    """Tiles of 16 and of 32 weight rows, eight and sixteen waves, ragged ends; gate and up."""
+    wq, ws = i8.rows(214, M, K, -128, 127)
+    xq, xs = i8.rows(215, N, K, -128, 127)
+    W, X = matrix(wq, ws), matrix(xq, xs)
+    ref = i8.product(wq, ws, xq, xs)
+    same(gq.gemm_i8(*W, *X), ref.astype(np.float64), "gemm")
+    U = matrix(wq[::-1].copy(), ws[::-1].copy())
+    g, u = ref.astype(np.float64), ref[:, ::-1].astype(np.float64)
+    a, _, p = i8.act(g, "silu")
+    tol = np.abs(a * u) * (i8.act_rel(p) + 2.0 ** -22) + np.abs(g * u) * 2.0 ** -125 + 2.0 ** -149
+    near(gq.gated_i8(W, U, *X), a * u, tol, "gated")
+
+
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("I,H,N", [(300, 130, 300), (1030, 128, 2050), (2048, 100, 4096), (2100, 129, 4097),
