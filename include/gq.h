@@ -645,8 +645,8 @@ size_t gq_gated_i8_backward_workspace_bytes(int64_t N, int64_t H, int64_t I);
 /* The whole gated feed-forward block over int8 weights, forward:
  *   h = round( act(W_gate v(x)) * W_up v(x) ), held in `type`;  out = W_down v(h),
  * v() the values gq_quantize_i8 leaves of each row.  h is rounded to the 16-bit type before
- * its codes are taken, as the expert layers hold it (with bfloat16 that rounding is about as
- * large as a third of a code's step at the largest values and smaller below).
+ * its codes are taken, as the expert layers hold it (with bfloat16 that rounding is at
+ * most half a code's step, at the largest values, and smaller below).
  * wq_gate, wq_up: I rows of H codes; wq_down: H rows of I codes.  x, out: [T][H] of `type`
  * (GQ_F16 or GQ_BF16).  A binary16 h above 65504 is infinite and its token's outputs NaN.  ws:
  * at least gq_ffn_i8_workspace_bytes() bytes, 16-byte aligned, contents on entry ignored; not
