@@ -567,8 +567,9 @@ gq_status gq_dequant_i8(const int8_t *q, int64_t ldq, const float *s, void *out,
  *   y[b][r] = sum_k w[r][k] * v(x)[b][k].
  * One row of K <= 16384, two of K <= 8192 and up to four of K <= 4096 are quantised by the
  * workgroups that multiply them, in one launch and without a workspace (wsp may be NULL); more
- * are quantised once, by a launch before, into wsp: at least gq_gemv_i8_workspace_bytes(K, B) bytes, 16-byte aligned, contents on entry
- * ignored; not to be in use by another call while this one runs.
+ * are quantised once, by a launch before, into wsp: at least gq_gemv_i8_workspace_bytes(K, B)
+ * bytes, 16-byte aligned, contents on entry ignored; not to be in use by another call while this
+ * one runs.
  * x: [B][K] and y: [B][M], both of `type` (any gq_dtype).  Requires K <= 131071, M <= 2^26,
  * ldw <= 2^22. */
 gq_status gq_gemv_i8(const int8_t *wq, int64_t ldw, const float *ws, const void *x, void *y,

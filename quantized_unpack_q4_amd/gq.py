@@ -835,13 +835,13 @@ def _i8_codes(name, q, dev):
     rows, K = q.shape
     if K < 1:
         raise ValueError("%s has rows of no codes" % name)
-    need = (K + 15) & -16
     ld, step = q.stride()
     if rows < 2: # (the stride of a dimension of one is anything)
-        ld = need
+        ld = (K + 15) & -16
     if (step != 1 and K > 1) or ld < K or ld & 15:
         raise ValueError("rows of %s must be contiguous and a multiple of 16 bytes apart" % name)
-    if rows and q.storage_offset() + (rows - 1) * ld + need > q.untyped_storage().nbytes():
+    if K & 15 and rows and (q.storage_offset() + (rows - 1) * ld + ((K + 15) & -16)
+                            > q.untyped_storage().nbytes()):
         raise ValueError("the storage of %s ends inside the 16 bytes of its last codes" % name)
     return q.data_ptr(), ld, rows, K
 
@@ -928,7 +928,8 @@ def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     xa = _mx_addr("x", x, dev, x.dtype)
     B = x.shape[0]
     y = _mx_new((B, M), x.dtype, x, stream) if out is None else out
-    need = lib().gq_gemv_i8_workspace_bytes(K, B)
+    # (up to four rows of K <= 4096 need none by the entry's contract: asking takes longer)
+    need = lib().gq_gemv_i8_workspace_bytes(K, B) if B > 4 or K > 4096 else 0
     _check(lib().gq_gemv_i8(qa, ld, sa, xa, _mx_addr("out", y, dev, x.dtype, (B, M)), code, M, K, B,
                             *_i8_wsp("wsp", wsp, need, x, dev, stream), _mx_stream(stream, dev)))
     return y
