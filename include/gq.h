@@ -628,10 +628,12 @@ gq_status gq_gated_i8(const int8_t *wq_gate, int64_t ld_gate, const float *ws_ga
  *   dg = dh * u * act'(g),  du = dh * act(g), formed in binary32 from g and u, which are
  *   computed again;
  *   dX[n][k] = round( sum_i dg[n][i] * w_gate[i][k] + du[n][i] * w_up[i][k] ).
- * dh: [N][I] and dx: [N][H], both of `type` (GQ_F16 or GQ_BF16).  The operands of these 16-bit
- * products are dg and du times the fraction f of their weight row's scale s = f 2^e
- * (1/2 <= f < 1), rounded to `type`, and the codes times 2^e, which are exact (in binary16 for
- * scales from 2^-25 to 2^8, else rounded); sums binary32, one rounding of the result.  ws: at least gq_gated_i8_backward_workspace_bytes() bytes, 16-byte aligned,
+ * dh: [N][I] and dx: [N][H], both of `type` (GQ_F16 or GQ_BF16).  The operands of the last
+ * products are dg and du times their weight row's scale and a power of two for each token, rounded
+ * to binary16 for both types, and the codes, which are exact; sums binary32, the power of two
+ * taken back, one rounding of the result.  The power of two keeps every operand of finite
+ * gradients within binary16: dg and du may be larger or smaller than `type` holds.  ws: at least
+ * gq_gated_i8_backward_workspace_bytes() bytes, 16-byte aligned,
  * contents on entry ignored; not to be in use by another call while this one runs.  Requires
  * the limits of gq_gated_i8, 1 <= I <= 2^21 and N*H <= 2^37. */
 gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const float *ws_gate,

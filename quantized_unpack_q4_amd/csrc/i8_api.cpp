@@ -148,8 +148,8 @@ gq_status gemm_backward_shape(const char *fn, int64_t M, int64_t K, int64_t N, i
     return GQ_OK;
 }
 
-// The gated half's: the gradients of g and u, rows of each so many elements apart; the sums of
-// the runs; total.
+// The gated half's: the gradients of g and u, rows of each so many elements apart; their
+// exponents (grad_exponents) and the sums of the runs; total.
 int64_t grad_ld(int64_t I) { return (I + 63) / 64 * 64; }
 gq_status gated_backward_shape(const char *fn, int64_t N, int64_t H, int64_t I, size_t off[3])
 {
@@ -376,7 +376,7 @@ gq_status gq_gated_i8_backward(const int8_t *wq_gate, int64_t ld_gate, const flo
     GQ_TRY(check_ptr(fn, "dh", dh));
     GQ_TRY(check_ptr(fn, "dx", dx));
     GQ_TRY(check_ws(fn, "ws", ws, ws_bytes, off[2]));
-    uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u, times the scales' fractions
+    uint16_t *d = (uint16_t *)ws; // [N][2][ldd]: of g, of u
     const int64_t ldd = grad_ld(I);
     const gq::I8Mat gate{wq_gate, ld_gate, ws_gate}, upm{wq_up, ld_up, ws_up};
     GQ_TRY(launched(fn, gq::launch_gated_grads_i8(gate, upm, {xq, ldx, xs}, dh, d, ldd, type, act, I,

@@ -215,22 +215,6 @@ __device__ __forceinline__ float i8_scaled(int sum, float ws, float xs)
     return as_is((float)sum * ws * xs);
 }
 
-// A weight row's scale as f P, P a power of two and f in [1/2, 1): codes times P are exact in
-// both 16-bit types (in binary16 for scales from 2^-25 to 2^8), so that where f can go into
-// the other operand before its rounding, a product rounds one operand only.  P stays between
-// 2^-126 and 2^127; what that leaves (zero, subnormal and the largest scales, infinity, NaN)
-// is f's.
-__device__ __forceinline__ float scale_pow2(float s)
-{
-    const uint32_t e = __builtin_bit_cast(uint32_t, s) & 0x7f800000u;
-    return __builtin_bit_cast(float, min(e + 0x00800000u, 0x7f000000u));
-}
-__device__ __forceinline__ float scale_fraction(float s)
-{
-    const uint32_t e = __builtin_bit_cast(uint32_t, scale_pow2(s)) >> 23;
-    return __builtin_amdgcn_ldexpf(s, 127 - (int)e);
-}
-
 // Four consecutive 16-bit values from element i (any alignment), of which n exist, as they lie,
 // and as binary32.
 __device__ __forceinline__ uint2 load4(const uint16_t *x, int64_t i, int64_t n)

@@ -15,6 +15,10 @@
 // same l, hold 128 consecutive columns, sixteen of them consecutive in a lane's accumulators,
 // which are stored as they lie.
 //
+// SCALED, for the gated half: d's rows hold the weights' scales and a power of two already
+// (i8_tiles.hip), the weights' operands are their codes, which both 16-bit types hold exactly, and
+// the power of two is taken back from the sums.
+//
 // Where tiles are too few to fill the device the sum is cut into runs, a workgroup each, whose
 // binary32 sums a second launch adds in run order.
 //
@@ -46,6 +50,7 @@ struct GradArgs {
     int nparts;
     int M, K, N; // d has zeros from M to the next multiple of 8
     int tiles_k, tiles_total;
+    const int *e;   // SCALED: the rows' exponents
     int splits;     // runs of the sum, a workgroup each
     float *partial; // their sums where there are several: [splits][N][ldp]
     int64_t ldp;
@@ -62,13 +67,15 @@ __device__ __forceinline__ float16_t mfma32_16(uint4 a, uint4 b, float16_t c)
                                                       __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
 }
 
-template <bool BF16, bool SPLIT, int WM, int WN, int FN, bool TAIL>
+// SCALED: operands are binary16 whatever the result's type.
+template <bool BF16, bool SCALED, int WM, int WN, int FN, bool TAIL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
 {
     constexpr int NW = WM * WN, NT = 64 * NW, BK = 128 * WM, BN = 32 * FN * WN;
     constexpr int UN = 8 * (BK / 4) / NT; // 8-row, 4-column units of a thread and stage
     constexpr int CX = BN / 8 / NW;       // 1 KB copies of d per wave and stage
     constexpr int kD = 2 * BK * 128;      // byte offset of d in LDS
+    constexpr bool OP_BF16 = BF16 && !SCALED; // type of the operands
     static_assert(UN * NT == 8 * (BK / 4) && CX * 8 * NW == BN, "whole units and copies");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (BK + BN) * 128];
     const TileWork work = tile_work(p.tiles_total * p.splits, p.tiles_total * p.splits);
@@ -160,14 +167,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     raw[u].w[i] = load_dword(wq, uoff[u][i]);
-                *reinterpret_cast<float4 *>(raw[u].s) = ldf4(wsc + urow[u]);
-                *reinterpret_cast<float4 *>(raw[u].s + 4) = ldf4(wsc + urow[u] + 4);
+                if constexpr (!SCALED) {
+                    *reinterpret_cast<float4 *>(raw[u].s) = ldf4(wsc + urow[u]);
+                    *reinterpret_cast<float4 *>(raw[u].s + 4) = ldf4(wsc + urow[u] + 4);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int m = min(urow[u] + i, left - 1);
                     raw[u].w[i] = load_dword(wq, (uint32_t)m * ld + (uint32_t)ucol[u]);
-                    raw[u].s[i] = wsc[m];
+                    if constexpr (!SCALED)
+                        raw[u].s[i] = wsc[m];
                 }
             }
         }
@@ -186,12 +196,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         for (int u = 0; u < UN; ++u)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                asm volatile("" : "+v"(raw[u].w[i]), "+v"(raw[u].s[i]));
-                if constexpr (BK == 256)
-                    raw[u].s[i] = __builtin_bit_cast(
-                        float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, raw[u].s[i])));
-                if constexpr (SPLIT)
-                    raw[u].s[i] = scale_pow2(raw[u].s[i]);
+                asm volatile("" : "+v"(raw[u].w[i]));
+                if constexpr (!SCALED) {
+                    asm volatile("" : "+v"(raw[u].s[i]));
+                    if constexpr (BK == 256)
+                        raw[u].s[i] = __builtin_bit_cast(
+                            float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, raw[u].s[i])));
+                }
             }
     };
     // Column i of the units into buffer b, in NM pieces, one after each product of a step: q s of
@@ -205,9 +216,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
 #pragma unroll
         for (int e = piece * PW; e < piece * PW + PW; ++e) {
             const int u = e / 8, j = e % 8;
-            const float v = as_is((float)(int8_t)(raw[u].w[j] >> (8 * i)) * raw[u].s[j]);
+            float v = (float)(int8_t)(raw[u].w[j] >> (8 * i));
+            if constexpr (!SCALED)
+                v = as_is(v * raw[u].s[j]);
             if (j % 2)
-                pk[i][j / 2] = mx_pack2<BF16>(pv[i], v);
+                pk[i][j / 2] = mx_pack2<OP_BF16>(pv[i], v);
             else
                 pv[i] = v;
             if (j == 7)
@@ -261,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                acc[i][j] = mfma32_16<BF16>(f.a[i], f.b[j], acc[i][j]);
+                acc[i][j] = mfma32_16<OP_BF16>(f.a[i], f.b[j], acc[i][j]);
                 asm volatile("" : "+v"(acc[i][j]));
                 between(i * FN + j);
                 __builtin_amdgcn_sched_barrier(0);
@@ -349,6 +362,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
             }
             continue;
         }
+        if constexpr (SCALED) {
+            const int e = p.e[n0 + n];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    acc[i][j][v] = as_is(__builtin_amdgcn_ldexpf(acc[i][j][v], e));
+        }
         uint16_t *out = p.dx + (int64_t)(n0 + n) * K;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -371,11 +392,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_tile_kernel(GradArgs p)
     }
 }
 
-// The runs' sums added in run order and rounded once.
+// The runs' sums added in run order, multiplied by 2^e of their row where there are such, and
+// rounded once.
 template <bool BF16>
 __global__ __launch_bounds__(256) void grad_sum_kernel(const float *__restrict__ partial, int splits,
-                                                       int64_t ldp, uint16_t *__restrict__ dx, int K,
-                                                       int64_t N)
+                                                       int64_t ldp, const int *__restrict__ e,
+                                                       uint16_t *__restrict__ dx, int K, int64_t N)
 {
     const int64_t row4 = (K + 3) / 4, total = N * row4, step = (int64_t)gridDim.x * 256;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += step) {
@@ -385,6 +407,11 @@ __global__ __launch_bounds__(256) void grad_sum_kernel(const float *__restrict__
         float4_t v = *reinterpret_cast<const float4_t *>(s);
         for (int i = 1; i < splits; ++i)
             v += *reinterpret_cast<const float4_t *>(s + i * N * ldp);
+        if (e) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                v[c] = as_is(__builtin_amdgcn_ldexpf(v[c], e[n]));
+        }
         mx_store4(dx, n * K + k, BF16 ? kBF16 : kF16, v, K - k, K % 4 == 0);
     }
 }
@@ -405,7 +432,7 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *__restr
     }
 }
 
-template <bool SPLIT, int WM, int WN, int FN>
+template <bool SCALED, int WM, int WN, int FN>
 hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
 {
     constexpr int BK = 128 * WM, BN = 32 * FN * WN;
@@ -413,7 +440,7 @@ hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
     p.tiles_total = p.tiles_k * ((p.N + BN - 1) / BN);
     const dim3 grid(tile_grid((int64_t)p.tiles_total * p.splits, (int64_t)p.tiles_total * p.splits)), block(64 * WM * WN);
     auto launch = [&](auto bf16, auto tail) {
-        hipLaunchKernelGGL((grad_tile_kernel<decltype(bf16)::value, SPLIT, WM, WN, FN, decltype(tail)::value>),
+        hipLaunchKernelGGL((grad_tile_kernel<decltype(bf16)::value, SCALED, WM, WN, FN, decltype(tail)::value>),
                            grid, block, 0, st, p);
     };
     if (type == kBF16)
@@ -459,13 +486,13 @@ GradPlan grad_plan(int nparts, int64_t M, int64_t K, int64_t N)
     return best;
 }
 
-template <bool SPLIT>
+template <bool SCALED>
 hipError_t launch_grad(const GradArgs &p, int tile, int type, hipStream_t st)
 {
     switch (tile) {
-    case 0: return launch_grad_tiles<SPLIT, 2, 4, 2>(p, type, st);
-    case 1: return launch_grad_tiles<SPLIT, 2, 4, 1>(p, type, st);
-    default: return launch_grad_tiles<SPLIT, 1, 2, 1>(p, type, st);
+    case 0: return launch_grad_tiles<SCALED, 2, 4, 2>(p, type, st);
+    case 1: return launch_grad_tiles<SCALED, 2, 4, 1>(p, type, st);
+    default: return launch_grad_tiles<SCALED, 1, 2, 1>(p, type, st);
     }
 }
 
@@ -485,10 +512,11 @@ hipError_t launch_align_rows(const uint16_t *d, int64_t ldd, uint16_t *out, int6
 size_t grad_partial_bytes(int nparts, int64_t M, int64_t K, int64_t N)
 {
     const int splits = grad_plan(nparts, M, K, N).splits;
-    return splits > 1 ? (size_t)splits * N * partial_ld(K) * 4 : 0;
+    const size_t e = nparts > 1 ? (size_t)grad_exponent_bytes(N) : 0;
+    return e + (splits > 1 ? (size_t)splits * N * partial_ld(K) * 4 : 0);
 }
 
-hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
+hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool scaled, int64_t ldd,
                           uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, void *partial,
                           hipStream_t st)
 {
@@ -503,19 +531,20 @@ hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64
     p.K = (int)K;
     p.N = (int)N;
     p.splits = plan.splits;
-    p.partial = (float *)partial;
+    p.e = scaled ? (const int *)partial : nullptr;
+    p.partial = (float *)((char *)partial + (scaled ? grad_exponent_bytes(N) : 0));
     p.ldp = partial_ld(K);
-    const hipError_t e = split ? launch_grad<true>(p, plan.tile, type, st)
-                               : launch_grad<false>(p, plan.tile, type, st);
+    const hipError_t e = scaled ? launch_grad<true>(p, plan.tile, type, st)
+                                : launch_grad<false>(p, plan.tile, type, st);
     if (e != hipSuccess || p.splits == 1)
         return e;
     const dim3 grid((unsigned)std::min((N * ((K + 3) / 4) + 255) / 256, (int64_t)1 << 14)), block(256);
     if (type == kBF16)
-        hipLaunchKernelGGL(grad_sum_kernel<true>, grid, block, 0, st, p.partial, p.splits, p.ldp, dx,
-                           (int)K, N);
+        hipLaunchKernelGGL(grad_sum_kernel<true>, grid, block, 0, st, p.partial, p.splits, p.ldp,
+                           p.e, dx, (int)K, N);
     else
-        hipLaunchKernelGGL(grad_sum_kernel<false>, grid, block, 0, st, p.partial, p.splits, p.ldp, dx,
-                           (int)K, N);
+        hipLaunchKernelGGL(grad_sum_kernel<false>, grid, block, 0, st, p.partial, p.splits, p.ldp,
+                           p.e, dx, (int)K, N);
     return hipGetLastError();
 }
 

@@ -40,25 +40,31 @@ hipError_t launch_gated_i8(I8Mat gate, I8Mat up, I8Mat x, void *h, int type, int
 // The same from 1 to 16 float rows x [N][H], x and h of `type`.
 hipError_t launch_gated_gemv_i8(I8Mat gate, I8Mat up, const void *x, void *h, int type, int act,
                                 int64_t I, int64_t H, int N, hipStream_t st);
-// The gradients of g and u for a gradient dh [N][I] of h, each times the fraction of its weight
-// row's scale (scale_fraction): d [N][2][ldd], of dh's 16-bit type, zeros from I to the next
-// multiple of 8.
+// The gradients of g and u for a gradient dh [N][I] of h (of `type`, 16 bits), each times its
+// weight row's scale and 2^-e, e a whole number for each of the N rows: d [N][2][ldd] in binary16,
+// zeros from I to the next multiple of 8, and e at grad_exponents(d, N, ldd).
 hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *dh, uint16_t *d,
                                  int64_t ldd, int type, int act, int64_t I, int64_t H, int64_t N,
                                  hipStream_t st);
+// Behind d, 256-byte aligned as seen from it.
+constexpr int64_t grad_exponent_bytes(int64_t N) { return (N * 4 + 255) / 256 * 256; }
+inline int *grad_exponents(uint16_t *d, int64_t N, int64_t ldd)
+{
+    return reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(d) + (N * 2 * ldd * 2 + 255) / 256 * 256);
+}
 
 // dx[n][k] = sum over the parts p and rows m < M of d_p[n][m] w16_p[m][k], w16 each weight
 // rounded to the 16-bit type of d and dx; rows of d are ldd elements apart, a multiple of 8, with
-// zeros from M to the next multiple of 8.  split: d holds the fractions of the scales already,
-// weights are codes times their powers of two.
+// zeros from M to the next multiple of 8.  scaled: d is launch_gated_grads_i8's, the weights are
+// the codes, and sums are multiplied by 2^e.
 struct I8GradPart {
     I8Mat w;
     const uint16_t *d;
 };
-// The sum may be cut into runs, whose sums then go through `partial`, this many bytes (zero: one
-// run).
+// The workspace `partial`, this many bytes: for two parts (scaled) it begins with the e's,
+// grad_exponent_bytes(N); the sum may be cut into runs, whose sums then go through the rest.
 size_t grad_partial_bytes(int nparts, int64_t M, int64_t K, int64_t N);
-hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool split, int64_t ldd,
+hipError_t launch_grad_i8(const I8GradPart *parts, int nparts, bool scaled, int64_t ldd,
                           uint16_t *dx, int type, int64_t M, int64_t K, int64_t N, void *partial,
                           hipStream_t st);
 

@@ -16,7 +16,10 @@
 //
 // Gate/up: half of a tile's weight rows are rows of the gate matrix, half the same rows of the
 // up matrix, and a wave holds both of a row: h, or the gradients of g and u, is formed in
-// registers: 14336 x 4096 by 1024 rows takes 116 us, with the gradients of g and u 128.
+// registers: 14336 x 4096 by 1024 rows takes 116 us, with the gradients of g and u 128.  Those
+// leave as binary16 operands of the product with the codes, times their weight row's scale and a
+// power of two of their token: 11 bits, where bfloat16 had 8, at the exponents a token's gradients
+// have, so that none leaves the type, as unscaled ones do (dg above 65504 for a dX of 100).
 //
 // The last stage of a K that is no multiple of 128: copies past a row's last 16 bytes repeat
 // those, and the weights' codes past K are zeroed in registers (what lies there in the
@@ -39,7 +42,8 @@ struct I8TileArgs {
     I8Mat w, w2; // gate/up: gate, up
     I8Mat x;
     void *y;
-    const uint16_t *dh; // kGrads
+    const uint16_t *dh; // kGrads: the gradient of h, of `type`
+    int *e;             // kGrads: exponents of the rows of y, which is binary16
     int64_t ldy;        // elements between rows of y
     int64_t part;       // kGrads: elements from the gradient of g to that of u
     int type, act;
@@ -57,15 +61,14 @@ __device__ __forceinline__ int16v mfma_i8(uint4 a, uint4 b, int16v c)
 // results are held.
 constexpr int store_groups(int MODE, int FM) { return MODE == kPlain ? 4 * FM : MODE == kGated ? 2 * FM : 4; }
 
-// After the stages LDS holds the waves' scratch for storing and, per weight row, the scales of
-// both matrices and their fractions.
+// After the stages LDS holds the waves' scratch for storing and, per weight row, the scales.
 constexpr int scratch_bytes(int MODE, int NW, int FM) { return NW * store_scratch(store_groups(MODE, FM), 4); }
 
 template <int MODE, int WM, int WN, int FM, int FN, int NB>
 constexpr int i8_lds_bytes()
 {
     constexpr int BM = 32 * FM * WM;
-    return std::max(NB * (BM + 32 * FN * WN) * 128, scratch_bytes(MODE, WM * WN, FM) + 4 * BM * 4);
+    return std::max(NB * (BM + 32 * FN * WN) * 128, scratch_bytes(MODE, WM * WN, FM) + BM * 4);
 }
 
 // The tile of weight rows m0 .. (of each matrix) and activation rows n0 ..: NB stages in LDS,
@@ -215,7 +218,7 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
         stage(whole, std::true_type{});
     wait_copies<0>();
 
-    // per weight row of the tile: the scales and, for gradients, their fractions
+    // per weight row of the tile: the scales, of gate and up one after another
     constexpr int G = store_groups(MODE, FM);
     float *const sc = reinterpret_cast<float *>(lds + scratch_bytes(MODE, NW, FM));
     for (int i = tid; i < BW; i += 64 * NW) {
@@ -225,10 +228,6 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
         if constexpr (PAIR) {
             const float us = in ? p.w2.s[m0 + i] : 0.0f;
             sc[BW + i] = us;
-            if constexpr (MODE == kGrads) {
-                sc[2 * BW + i] = scale_fraction(ws);
-                sc[3 * BW + i] = scale_fraction(us);
-            }
         }
     }
     __syncthreads();
@@ -251,7 +250,7 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
     auto store = [&](const float4_t(&v)[G], void *y, int64_t n, int left, int64_t m) {
         if (MODE != kGrads && p.type == kF32)
             store_rows<kF32>(scr, y, n, left, m, end, v, p.ldy);
-        else if (p.type == kF16)
+        else if (MODE == kGrads || p.type == kF16)
             store_rows<kF16>(scr, y, n, left, m, end, v, p.ldy);
         else
             store_rows<kBF16>(scr, y, n, left, m, end, v, p.ldy);
@@ -264,6 +263,7 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
             break;
         const int64_t nr = n0 + min(n + r, nv - 1);
         const float xs = p.x.s[nr];
+        const int e = MODE == kGrads ? p.e[nr] : 0;
         // all of a row's gradients of h at once: one wait for memory instead of one a piece
         uint2 dh[MODE == kGrads ? 4 * FW : 1];
         if constexpr (MODE == kGrads) {
@@ -284,24 +284,24 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
 #pragma unroll
             for (int v4 = 0; v4 < 4; ++v4) {
                 const float *row = sc + mw + 32 * i + 8 * v4 + 4 * h;
-                const float4_t g = scaled4(i, j, v4, *reinterpret_cast<const float4_t *>(row), xs);
+                const float4_t ws = *reinterpret_cast<const float4_t *>(row);
+                const float4_t g = scaled4(i, j, v4, ws, xs);
                 if constexpr (MODE == kPlain) {
                     v[4 * i + v4] = g;
                 } else {
-                    const float4_t u = scaled4(FW + i, j, v4, *reinterpret_cast<const float4_t *>(row + BW), xs);
+                    const float4_t us = *reinterpret_cast<const float4_t *>(row + BW);
+                    const float4_t u = scaled4(FW + i, j, v4, us, xs);
                     if constexpr (MODE == kGated) {
                         v[4 * i + v4] = float4_t{gated_value(g[0], u[0], p.act), gated_value(g[1], u[1], p.act),
                                                  gated_value(g[2], u[2], p.act), gated_value(g[3], u[3], p.act)};
                     } else {
-                        const float4_t fg = *reinterpret_cast<const float4_t *>(row + 2 * BW);
-                        const float4_t fu = *reinterpret_cast<const float4_t *>(row + 3 * BW);
                         const float4_t d = values4(dh[4 * i + v4], p.type);
                         float4_t dg, du;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const Gate a = gate_grad(g[c], p.act);
-                            dg[c] = d[c] * u[c] * a.da * fg[c];
-                            du[c] = d[c] * a.a * fu[c];
+                            dg[c] = __builtin_amdgcn_ldexpf(d[c] * u[c] * a.da * ws[c], -e);
+                            du[c] = __builtin_amdgcn_ldexpf(d[c] * a.a * us[c], -e);
                         }
                         v[v4] = dg;
                         v2[v4] = du;
@@ -317,6 +317,73 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
         }
         if constexpr (MODE != kGrads)
             store(v, p.y, n0 + n, nv - n, m);
+    }
+}
+
+// The exponent e of each row of gradients, so that dg ws 2^-e and du us 2^-e, the operands of the
+// product after this one, are binary16 numbers: with |act'| < 1.13, |act(g)| <= |g| and
+// |sum| <= 128 L, L the sum of the row's magnitudes of codes, both are at most
+// 1.13 max_i |dh[i] ws[i] us[i]| |xs| 128 L, and e makes that, taken by the factors' exponents, at
+// most 2^15.  The bound exceeds what a row really holds, by some 2^13 for sums of codes of both
+// signs: the largest operands are then near 2^2, all that are down to 2^-16 of them have their 11
+// bits, and smaller ones an error of 2^-27 of them.  A workgroup per row; 1024 rows of 14336
+// gradients 12 us.
+template <int TYPE>
+__global__ __launch_bounds__(256) void grad_exponents_kernel(I8TileArgs p)
+{
+    __shared__ uint32_t part[2][4];
+    const int tid = threadIdx.x;
+    const int64_t n = blockIdx.x;
+    // |v| < 2^(field(v) - 126)
+    auto field = [](float v) { return __builtin_bit_cast(uint32_t, v) >> 23 & 0xffu; };
+    uint32_t top = 0; // of the three factors' fields
+    for (int i = 8 * tid; i < p.M; i += 8 * 256) {
+        const int left = p.M - i;
+        I8Load8<TYPE> d;
+        d.load(p.dh, n * p.M + i, min(left, 8));
+        float s[8], t[8];
+        if (left >= 8) {
+            *reinterpret_cast<float4 *>(s) = ldf4(p.w.s + i);
+            *reinterpret_cast<float4 *>(s + 4) = ldf4(p.w.s + i + 4);
+            *reinterpret_cast<float4 *>(t) = ldf4(p.w2.s + i);
+            *reinterpret_cast<float4 *>(t + 4) = ldf4(p.w2.s + i + 4);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[j] = j < left ? p.w.s[i + j] : 0.0f;
+                t[j] = j < left ? p.w2.s[i + j] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            top = max(top, field(d.value(j)) + field(s[j]) + field(t[j]));
+    }
+    uint32_t sum = 0;
+    const int8_t *q = p.x.q + n * p.x.ld;
+    for (int k = 16 * tid; k < p.K; k += 16 * 256) {
+        const uint4 v = ld16(q + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { // codes past K count as zeros
+            const int c = min(max(p.K - k - 4 * j, 0), 4);
+            const uint32_t mask = c == 4 ? ~0u : (1u << (8 * c)) - 1u;
+            sum = __builtin_amdgcn_sad_u8((w[j] & mask) ^ 0x80808080u, 0x80808080u, sum);
+        }
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        sum += __shfl_xor(sum, off, 64);
+    const uint32_t m = wave_max(top);
+    if ((tid & 63) == 0) {
+        part[0][tid >> 6] = m;
+        part[1][tid >> 6] = sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const int most = (int)max(max(part[0][0], part[0][1]), max(part[0][2], part[0][3]));
+        const uint32_t l = part[1][0] + part[1][1] + part[1][2] + part[1][3];
+        const int e = most + (int)field(p.x.s[n]) + (int)field((float)l) - 5 * 126 + 8 - 15;
+        p.e[n] = max(e, -100); // (rows of zeros, or of next to nothing)
     }
 }
 
@@ -447,6 +514,7 @@ hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *
     p.x = x;
     p.y = d;
     p.dh = dh;
+    p.e = grad_exponents(d, N, ldd);
     p.ldy = 2 * ldd;
     p.part = ldd;
     p.type = type;
@@ -454,7 +522,12 @@ hipError_t launch_gated_grads_i8(I8Mat gate, I8Mat up, I8Mat x, const uint16_t *
     p.M = (int)I;
     p.K = (int)H;
     p.N = (int)N;
-    return launch_pair<kGrads>(p, st);
+    if (type == kBF16)
+        hipLaunchKernelGGL(grad_exponents_kernel<kBF16>, dim3((unsigned)N), dim3(256), 0, st, p);
+    else
+        hipLaunchKernelGGL(grad_exponents_kernel<kF16>, dim3((unsigned)N), dim3(256), 0, st, p);
+    const hipError_t err = hipGetLastError();
+    return err != hipSuccess ? err : launch_pair<kGrads>(p, st);
 }
 
 } // namespace gq
