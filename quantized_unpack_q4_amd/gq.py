@@ -872,12 +872,14 @@ def _rows_2d(name, x):
 
 
 def _i8_wsp(name, wsp, need, like, dev, stream):
-    """(address, bytes) of a workspace that some sizes need, a new one where none is given."""
+    """(address, bytes, tensor) of a workspace that some sizes need, a new one where none is given.
+    The tensor is to be held until the call has returned: it launches several kernels, and other
+    threads may allocate between them."""
     if wsp is None:
         if not need:
-            return 0, 0
+            return 0, 0, None
         wsp = _mx_new((need,), _torch.uint8, like, stream)
-    return _mx_addr(name, wsp, dev, wsp.dtype), wsp.numel() * wsp.element_size()
+    return _mx_addr(name, wsp, dev, wsp.dtype), wsp.numel() * wsp.element_size(), wsp
 
 
 def quantize_i8(x, out=None, stream=None):
@@ -930,8 +932,9 @@ def gemv_i8(wq, ws, x, wsp=None, out=None, stream=None):
     y = _mx_new((B, M), x.dtype, x, stream) if out is None else out
     # (up to four rows of K <= 4096 need none by the entry's contract: asking takes longer)
     need = lib().gq_gemv_i8_workspace_bytes(K, B) if B > 4 or K > 4096 else 0
+    wa, wbytes, wsp = _i8_wsp("wsp", wsp, need, x, dev, stream)
     _check(lib().gq_gemv_i8(qa, ld, sa, xa, _mx_addr("out", y, dev, x.dtype, (B, M)), code, M, K, B,
-                            *_i8_wsp("wsp", wsp, need, x, dev, stream), _mx_stream(stream, dev)))
+                            wa, wbytes, _mx_stream(stream, dev)))
     return y
 
 
@@ -964,10 +967,10 @@ def gemm_i8_backward(wq, ws, dy, wsp=None, out=None, stream=None):
         raise ValueError("dY has rows of %d values, expected %d" % (MD, M))
     dx = _mx_new((N, K), dy.dtype, dy, stream) if out is None else out
     need = lib().gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd)
+    pa, pbytes, wsp = _i8_wsp("wsp", wsp, need, dy, dev, stream)
     _check(lib().gq_gemm_i8_backward(wa, ldw, wsa, dy.data_ptr(), ldd,
                                      _mx_addr("out", dx, dev, dy.dtype, (N, K)), code, M, K, N,
-                                     *_i8_wsp("wsp", wsp, need, dy, dev, stream),
-                                     _mx_stream(stream, dev)))
+                                     pa, pbytes, _mx_stream(stream, dev)))
     return dx
 
 
