@@ -206,8 +206,10 @@ __global__ __launch_bounds__(64 * W) void i8_stream_kernel(I8StreamArgs p)
             }
             const float xs = FLOATS ? xscale[b] : p.xc.s[b];
             float v = i8_scaled(sum[0], p.w.s[row], xs);
-            if constexpr (PAIR)
-                v = gated_value(v, i8_scaled(sum[P - 1], p.w2.s[row], xs), p.act);
+            if constexpr (PAIR) {
+                const float u = i8_scaled(sum[P - 1], p.w2.s[row], xs);
+                v = p.type == kF32 ? gated_value<true>(v, u, p.act) : gated_value<false>(v, u, p.act);
+            }
             i8_store(p.y, (int64_t)b * M + row, p.type, v);
         }
         __syncthreads();

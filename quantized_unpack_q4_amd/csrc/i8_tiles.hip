@@ -279,42 +279,48 @@ __device__ __forceinline__ void i8_tile(const I8TileArgs &p, int m0, int n0, uin
             }
         }
         float4_t v[G], v2[MODE == kGrads ? G : 1];
+        auto form = [&](auto f32) {
+            auto value = [&](float g, float u) { return gated_value<decltype(f32)::value>(g, u, p.act); };
 #pragma unroll
-        for (int i = 0; i < FW; ++i) {
+            for (int i = 0; i < FW; ++i) {
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-                const float *row = sc + mw + 32 * i + 8 * v4 + 4 * h;
-                const float4_t ws = *reinterpret_cast<const float4_t *>(row);
-                const float4_t g = scaled4(i, j, v4, ws, xs);
-                if constexpr (MODE == kPlain) {
-                    v[4 * i + v4] = g;
-                } else {
-                    const float4_t us = *reinterpret_cast<const float4_t *>(row + BW);
-                    const float4_t u = scaled4(FW + i, j, v4, us, xs);
-                    if constexpr (MODE == kGated) {
-                        v[4 * i + v4] = float4_t{gated_value(g[0], u[0], p.act), gated_value(g[1], u[1], p.act),
-                                                 gated_value(g[2], u[2], p.act), gated_value(g[3], u[3], p.act)};
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    const float *row = sc + mw + 32 * i + 8 * v4 + 4 * h;
+                    const float4_t ws = *reinterpret_cast<const float4_t *>(row);
+                    const float4_t g = scaled4(i, j, v4, ws, xs);
+                    if constexpr (MODE == kPlain) {
+                        v[4 * i + v4] = g;
                     } else {
-                        const float4_t d = values4(dh[4 * i + v4], p.type);
-                        float4_t dg, du;
+                        const float4_t us = *reinterpret_cast<const float4_t *>(row + BW);
+                        const float4_t u = scaled4(FW + i, j, v4, us, xs);
+                        if constexpr (MODE == kGated) {
+                            v[4 * i + v4] = float4_t{value(g[0], u[0]), value(g[1], u[1]), value(g[2], u[2]), value(g[3], u[3])};
+                        } else {
+                            const float4_t d = values4(dh[4 * i + v4], p.type);
+                            float4_t dg, du;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const Gate a = gate_grad(g[c], p.act);
-                            dg[c] = __builtin_amdgcn_ldexpf(d[c] * u[c] * a.da * ws[c], -e);
-                            du[c] = __builtin_amdgcn_ldexpf(d[c] * a.a * us[c], -e);
+                            for (int c = 0; c < 4; ++c) {
+                                const Gate a = gate_grad(g[c], p.act);
+                                dg[c] = __builtin_amdgcn_ldexpf(d[c] * u[c] * a.da * ws[c], -e);
+                                du[c] = __builtin_amdgcn_ldexpf(d[c] * a.a * us[c], -e);
+                            }
+                            v[v4] = dg;
+                            v2[v4] = du;
                         }
-                        v[v4] = dg;
-                        v2[v4] = du;
+                    }
+                }
+                if constexpr (MODE == kGrads) {
+                    if (m + 32 * i < M) {
+                        store(v, p.y, n0 + n, nv - n, m + 32 * i);
+                        store(v2, reinterpret_cast<uint16_t *>(p.y) + p.part, n0 + n, nv - n, m + 32 * i);
                     }
                 }
             }
-            if constexpr (MODE == kGrads) {
-                if (m + 32 * i < M) {
-                    store(v, p.y, n0 + n, nv - n, m + 32 * i);
-                    store(v2, reinterpret_cast<uint16_t *>(p.y) + p.part, n0 + n, nv - n, m + 32 * i);
-                }
-            }
-        }
+        };
+        if (MODE == kGated && p.type == kF32)
+            form(std::true_type{});
+        else
+            form(std::false_type{});
         if constexpr (MODE != kGrads)
             store(v, p.y, n0 + n, nv - n, m);
     }
