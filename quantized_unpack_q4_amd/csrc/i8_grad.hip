@@ -37,6 +37,7 @@
 #include "gq_internal.h"
 #include "gq_lds_dma.h"
 #include "i8_device.h"
+#include "i8_plan.h"
 #include "mxfp4_tile.h"
 
 namespace gq {
@@ -448,42 +449,6 @@ hipError_t launch_grad_tiles(GradArgs p, int type, hipStream_t st)
     else
         p.M % 64 ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
     return hipGetLastError();
-}
-
-struct GradTile {
-    int columns, rows, per_cu; // of a tile, and tiles a CU holds
-    double stage;              // us a stage takes
-};
-constexpr GradTile kTiles[] = {{256, 256, 1, 1.7}, {256, 128, 1, 1.2}, {128, 64, 3, 1.0}};
-
-struct GradPlan {
-    int tile, splits;
-};
-// The tile and the number of runs with the least estimated time: rounds of workgroups on the
-// device's 256 CUs, 4 us for a workgroup's start and end; runs add a launch and the traffic of
-// their sums.  Measured, us (tiles of 256 x 256, 256 x 128, 128 x 64, with the best number of runs):
-// 4096 x 4096 by 16 rows 17 (16 runs), 15 (16), 15 (8); by 130 rows 31 (16), 28 (8), 27 (8), in one
-// run 93, 65, 58; by 512 rows 48 (4), 40 (4), 51 (4); 14336 x 4096 by 2048 rows 228 (2), 248 (1),
-// 402 (4).
-GradPlan grad_plan(int nparts, int64_t M, int64_t K, int64_t N)
-{
-    constexpr int64_t kCus = 256;
-    const int64_t stages = nparts * ((M + 63) / 64);
-    GradPlan best{};
-    double least = 1e30;
-    for (int i = 0; i < 3; ++i) {
-        const GradTile &t = kTiles[i];
-        const int64_t tiles = (K + t.columns - 1) / t.columns * ((N + t.rows - 1) / t.rows);
-        for (int s = 1; s <= 16 && s <= stages; ++s) {
-            const int64_t rounds = (tiles * s + kCus * t.per_cu - 1) / (kCus * t.per_cu);
-            double us = (double)rounds * ((double)((stages + s - 1) / s) * t.stage + 4.0);
-            if (s > 1)
-                us += 3.0 + (double)(s * N * K) * 8.0 / 4e6;
-            if (us < least)
-                least = us, best = {i, s};
-        }
-    }
-    return best;
 }
 
 template <bool SCALED>

@@ -30,6 +30,7 @@
 #include "gq_internal.h"
 #include "gq_lds_dma.h"
 #include "i8_device.h"
+#include "i8_plan.h"
 #include "mxfp4_tile.h"
 
 namespace gq {
@@ -434,38 +435,10 @@ hipError_t launch_tiles(I8TileArgs p, hipStream_t st)
     return hipGetLastError();
 }
 
-// The tile for a shape, from an estimate of its time: stages (128 columns) in full rounds of
-// tiles on the device and a last one by how many CUs it has, and what a round takes besides.
-// Measured, us for K 14336 (112 stages): 64 x 64 tiles 26 up to one per CU, 46 at two, 92 at
-// four; 128 x 128 47 alone, 66 at one per CU; 256 x 256 67 for a lone round in halves, 194 a full
-// round.  So 4096 x 14336 takes by 130 rows 26 us on the first (47, 67 on the others), by 1024
-// rows 66 on the second (93, 81), by 4096 rows 194 on the third (356, 252); 1003 x 2048 by 77
-// rows 6.2, 11.3 and 14.5, 4096 x 512 by 1024 rows 9.9, 8.1 and 8.8.  Gate/up, whose smallest
-// tiles are 128 x 64: 14336 x 4096 by 64 rows 21, 28 and 29, by 130 rows 44, 47 and 37.
-int tile_choice(int64_t M, int64_t K, int64_t N, bool pair)
-{
-    const int64_t cus = device_cus();
-    const double st = (double)((K + 127) / 128);
-    auto tiles = [&](int64_t m, int64_t n) { return (M + m - 1) / m * ((N + n - 1) / n); };
-    auto last = [&](int64_t rest, double lone, double full) {
-        return rest ? lone + (full - lone) * (double)rest / (double)cus : 0;
-    };
-    auto rounds = [&](int64_t t) { return 2.5 * (double)((t + cus - 1) / cus); };
-    const int64_t t2 = tiles(128, 128), t3 = tiles(256, 256), whole = tiles_whole(t3, cus);
-    const double per_cu = (double)(pair ? tiles(128, 64) : tiles(64, 64)) / (double)cus;
-    const double more = std::max(0.0, per_cu - 1.0);
-    const double t64 = st * (pair ? 0.25 + 0.3 * std::min(per_cu, 1.0) + 0.4 * more : 0.2 + 0.195 * more) + 1.1 * more;
-    const double t128 = st * (0.58 * (double)(t2 / cus) + last(t2 % cus, 0.42, 0.58)) + rounds(t2);
-    const double t256 = st * (1.72 * (double)(t3 / cus) +
-                              (whole < t3 ? last(2 * (t3 - whole), 0.6, 1.15) : last(t3 % cus, 1.2, 1.72))) +
-                        rounds(t3);
-    return t64 <= t128 && t64 <= t256 ? 64 : t128 <= t256 ? 128 : 256;
-}
-
 template <int MODE>
 hipError_t launch_pair(const I8TileArgs &p, hipStream_t st)
 {
-    switch (tile_choice(2 * (int64_t)p.M, p.K, p.N, true)) {
+    switch (i8_tile_choice(2 * (int64_t)p.M, p.K, p.N, true, device_cus())) {
     case 64: return launch_tiles<MODE, 2, 2, 2, 1, 3>(p, st);
     case 128: return launch_tiles<MODE, 2, 2, 2, 2, 3>(p, st);
     default: return launch_tiles<MODE, 2, 4, 4, 2, 2>(p, st);
@@ -486,7 +459,7 @@ hipError_t launch_i8_tiles(I8Mat w, I8Mat x, void *y, int type, int64_t M, int64
     p.M = (int)M;
     p.K = (int)K;
     p.N = (int)N;
-    switch (tile_choice(M, K, N, false)) {
+    switch (i8_tile_choice(M, K, N, false, device_cus())) {
     case 64: return launch_tiles<kPlain, 2, 2, 1, 1, 4>(p, st);
     case 128: return launch_tiles<kPlain, 2, 2, 2, 2, 3>(p, st);
     default: return launch_tiles<kPlain, 2, 4, 4, 2, 2>(p, st);

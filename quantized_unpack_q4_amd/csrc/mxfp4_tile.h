@@ -4,6 +4,7 @@
 #include "gq_lds_dma.h"
 #include "mxfp4_device.h"
 #include "mxfp4_krun.h"
+#include "tile_rounds.h"
 
 namespace gq {
 
@@ -36,17 +37,6 @@ __device__ __forceinline__ TileWork tile_work(int total, int whole)
         return {-1, -1};
     return cut ? TileWork{whole + t / 2, t & 1} : TileWork{t, -1};
 }
-// How many of the tiles are not cut, and the workgroups of the launch.
-inline int tiles_whole(int64_t total, int64_t cus)
-{
-    const int64_t rest = total % cus;
-    return (int)(rest > 0 && 2 * rest <= cus ? total - rest : total);
-}
-inline unsigned tile_grid(int64_t total, int64_t whole)
-{
-    return (unsigned)((whole + 7) / 8 * 8 + (2 * (total - whole) + 7) / 8 * 8);
-}
-
 // Tile (tm, tn) number t: in groups of eight tile rows, columns one after another.
 __device__ __forceinline__ void tile_pos(int t, int tiles_m, int tiles_n, int &tm, int &tn)
 {
