@@ -25,7 +25,8 @@ def want_and_tolerance(gate, up, xq, xs, d64, kind, t):
     half a step of 11 bits, or 2^-25 scaled back, 2^-25 2^-15 2^6 of that bound."""
     g, u, (a, da, p) = gated_reference(gate, up, xq, xs, kind)
     sg, su = gate[1].astype(np.float64), up[1].astype(np.float64)
-    dg, du = d64 * u * da * sg, d64 * a * su
+    raw = d64 * u * da
+    dg, du = raw * sg, d64 * a * su
     sig = np.where(g != 0, a / np.where(g != 0, g, 1), 0.5)
     terms = np.abs(sig) + np.abs(da - sig) * 2
     eg = np.abs(d64 * u * sg) * terms * (2 * i8.act_rel(p) + 8 * 2.0 ** -24)
@@ -36,7 +37,7 @@ def want_and_tolerance(gate, up, xq, xs, d64, kind, t):
     qg, qu = gate[0].astype(np.float64), up[0].astype(np.float64)
     want = dg @ qg + du @ qu
     size = (np.abs(dg) + eg) @ np.abs(qg) + (np.abs(du) + eu) @ np.abs(qu)
-    return want, eg @ np.abs(qg) + eu @ np.abs(qu) + grad_tolerance(size, 2 * dg.shape[1], want, t), dg / sg
+    return want, eg @ np.abs(qg) + eu @ np.abs(qu) + grad_tolerance(size, 2 * dg.shape[1], want, t), raw
 
 
 def check(gate, up, xq, xs, dh, d64, kind, t):
