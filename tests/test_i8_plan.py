@@ -99,3 +99,27 @@ def test_product_tiles_at_their_measured_sizes(ask):
              (28672, 4096, 130, 1): 256}
     got = [t for t, _ in ask([("tile", *s, 256) for s in named])]
     assert got == list(named.values())
+
+
+def test_every_form_of_the_tiles_is_tested(ask):
+    """The sizes of tests/test_gpu_i8_tiles.py take the tiles they name, and leave none out."""
+    from tests import test_gpu_i8_tiles as sizes
+
+    def lie(rows, N): # of 256-row tiles on 256 CUs
+        tiles = -(-rows // 256) * -(-N // 256)
+        rest = tiles % 256
+        cut = rest if rest and 2 * rest <= 256 else 0
+        return "whole" if not cut else "halves" if cut == tiles else "both"
+
+    for cases, rows in ((sizes.PRODUCTS, 1), (sizes.GATED, 2)):
+        got = ask([("tile", rows * M, K, N, rows - 1, 256) for M, K, N in cases])
+        for (M, K, N), (tile, _) in zip(cases, got):
+            assert N > 16 and cases[M, K, N] == (tile, K % 128 == 0, lie(rows * M, N) if tile == 256 else None)
+        forms = set(cases.values())
+        assert forms == {(t, e, None) for t in (64, 128) for e in (False, True)} | {
+            (256, e, l) for e in (False, True) for l in ("whole", "halves", "both")}
+    for cases, parts in ((sizes.GRADIENTS, 1), (sizes.GATED_GRADIENTS, 2)):
+        got = ask([("grad", parts, *s) for s in cases])
+        for (M, K, N), (tile, runs) in zip(cases, got):
+            assert cases[M, K, N] == (tile, M % 64 == 0, runs > 1), (M, K, N, tile, runs)
+        assert set(cases.values()) == {(t, e, r) for t in range(3) for e in (False, True) for r in (False, True)}
