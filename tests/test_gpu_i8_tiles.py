@@ -112,3 +112,36 @@ def test_gemm_backward(M, K, N, t):
     got = gq.gemm_i8_backward(*matrix(wq, ws, extra=1), dy)
     near(got[dev(n)], want, tol, "dX")
     assert bool((got == gq.gemm_i8_backward(*matrix(wq, ws, extra=1), dy)).all())
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 7, 40, 200, 1000])
+def test_gradients_of_a_row_alone(N, t):
+    """A token's gradients alone and among others: the same but for the order of the sums, and with
+    others' infinities beside it not different at all."""
+    M, K = 300, 500
+    wq, ws = i8.rows(311, M, K)
+    W, dy = matrix(wq, ws), floats(312, N, M, t)[0]
+    gate, up = matrix(*i8.rows(313, M, K)), matrix(*i8.rows(314, M, K))
+    xq, xs = i8.rows(315, N, K)
+    n = N // 2
+    w = i8.weights16(wq, ws, t)
+    d64 = values(dy)
+    all_ = values(gq.gemm_i8_backward(*W, dy))
+    one = values(gq.gemm_i8_backward(*W, dy[n:n + 1].clone()))[0]
+    want = d64[n] @ w
+    # each within its tolerance of the formula
+    tol = grad_tolerance(np.abs(d64[n]) @ np.abs(w), M, want, t)
+    assert (np.abs(all_[n] - want) <= tol).all() and (np.abs(one - want) <= tol).all()
+    X = matrix(xq, xs)
+    gall = values(gq.gated_i8_backward(gate, up, *X, dy)[0])
+    gone = values(gq.gated_i8_backward(gate, up, *matrix(xq[n:n + 1], xs[n:n + 1]), dy[n:n + 1].clone())[0])
+    gw, gt, _ = want_and_tolerance(i8.rows(313, M, K), i8.rows(314, M, K), xq[n:n + 1], xs[n:n + 1],
+                                   d64[n:n + 1], "silu", t)
+    assert (np.abs(gall[n] - gw[0]) <= gt[0]).all() and (np.abs(gone - gw) <= gt).all()
+    if N > 1:
+        others = dy.clone()
+        others[n + 1:] = float("inf")
+        others[:n] = float("nan")
+        assert (values(gq.gemm_i8_backward(*W, others))[n] == all_[n]).all()
+        assert (values(gq.gated_i8_backward(gate, up, *X, others)[0])[n] == gall[n]).all()
