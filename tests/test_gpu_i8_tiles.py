@@ -145,3 +145,34 @@ def test_gradients_of_a_row_alone(N, t):
         others[:n] = float("nan")
         assert (values(gq.gemm_i8_backward(*W, others))[n] == all_[n]).all()
         assert (values(gq.gated_i8_backward(gate, up, *X, others)[0])[n] == gall[n]).all()
+
+
+def test_gradients_past_4_gib_of_codes():
+    """Gradients of a few weight rows at both ends of a matrix and around its 2^32-byte border, zeros
+    elsewhere: a wrong address shows whole, sums of a million rows do not hide it."""
+    torch = torch_cuda()
+    M, K, N = 1 << 20, 4160, 5
+    W = torch.empty((M, K), dtype=torch.int8, device="cuda").random_(-128, 128)
+    s = torch.empty(M, device="cuda").uniform_(2.0 ** -12, 2.0 ** -9)
+    border = (1 << 32) // K
+    rows = np.unique([*range(8), *range(border - 8, border + 9), *range((1 << 31) // K - 4, (1 << 31) // K + 5),
+                      *range(M // 2, M // 2 + 3), *range(M - 8, M)])
+    at = dev(rows)
+    for t in ("f16", "bf16"):
+        dy = torch.zeros((N, M), dtype=ttype(t), device="cuda")
+        d, d64 = floats(316, N, rows.size, t)
+        dy[:, at] = d
+        w = i8.weights16(W[at].cpu().numpy(), s[at].cpu().numpy(), t)
+        want, size = d64 @ w, np.abs(d64) @ np.abs(w)
+        tol = grad_tolerance(size, rows.size, want, t) # (products with zero add nothing)
+        assert (tol < np.abs(want)).mean() > 0.9 # (a result of zeros would fail)
+        near(gq.gemm_i8_backward(W, s, dy), want, tol, "dX")
+        # one row at a time, one token each: the row itself
+        for r in (0, border, border + 1, M - 1):
+            dy.zero_()
+            dy[3, r] = 1.0
+            got = values(gq.gemm_i8_backward(W, s, dy))
+            i = int(np.searchsorted(rows, r))
+            assert (got[3] == w[i]).all() and (got[[0, 1, 2, 4]] == 0).all(), r
+    del W, dy
+    torch.cuda.empty_cache()
