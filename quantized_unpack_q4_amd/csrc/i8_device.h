@@ -139,7 +139,7 @@ struct I8Load8<kF32> {
 };
 
 // The code of x, exactly.  The quotient lies between two halves of codes; h is the one nearer to
-// it, and 254 x - 2 h top decides on which side of h it is: 2 h is odd and at most 253, so
+// it, and 254 x - 2 h top decides on which side of h it is: 2 h is odd and at most 255, so
 // 2 h top is p + e of two binary32 numbers, and 254 x - p is exact where the two are close
 // (elsewhere its sign is).  x and top are scaled so that none of it overflows or vanishes.
 __device__ __forceinline__ int i8_code_exact(float x, float top)

@@ -3,9 +3,15 @@
 // scale = max|x| / 127, code = 127 x / max|x| to the nearest (i8_device.h).  A row with an
 // infinity or a NaN has a NaN scale and zero codes; a zero row has scale zero.
 //
-// Both move bytes and little else.  The quantiser reads a row once: a workgroup holds it in
-// registers, 16 values (one 16-byte store of codes) a thread, up to 16384 values; longer rows
-// are read twice.
+// Both move bytes and little else.  A workgroup of T threads quantises a row and holds 16 T values
+// of it in registers, 16 (one 16-byte store of codes) a thread; the rest of a longer row is read
+// twice, from a cache the second time.  T goes by the row's length, up to 256 (4096 values); rows
+// longer than that get 1024 threads, 16384 values, where no more than a row a CU is there
+// to hide the second reading: by 256 rows of 14336 bfloat16 values 6.0 us (with 256 threads 9.5), of
+// 8192 5.0 (5.9), 16 rows of 5000 4.9 (6.0).  With more rows the small workgroups, which wait less
+// for each other, make up for it: by 4096 rows of 14336 40.8 us (45.9 with 1024 threads), of 8192 21.8
+// (35.9), by 1024 of 14336 13.7 (15.5); from 257 to 512 of 14336 it is the other way round by up to a
+// fifth, 9.5 (7.8) to 10.1 (9.6), and by 1024 rows of 60000, past what either holds, 50 (43).
 #include "gq_internal.h"
 #include "i8_device.h"
 
@@ -156,7 +162,7 @@ hipError_t quantize(const void *x, int64_t ldx, int8_t *q, int64_t ldq, float *s
         hipLaunchKernelGGL((quantize_i8_kernel<TYPE, T>), grid, dim3(T), 0, st, x, ldx, q, ldq, s, N, K);
         return hipGetLastError();
     };
-    using std::integral_constant;
+    using std::integral_constant; // (1024 threads: see above)
     return K <= 1024              ? launch(integral_constant<int, 64>{})
            : K <= 2048            ? launch(integral_constant<int, 128>{})
            : K <= 4096 || N > 256 ? launch(integral_constant<int, 256>{})
