@@ -591,7 +591,9 @@ gq_status gq_gemm_i8(const int8_t *wq, int64_t ldw, const float *ws, const int8_
  * to codes passes gradients unchanged), for training what feeds quantised layers:
  *   dX[n][k] = round( sum_m dY[n][m] * w16[m][k] ), sums binary32, one rounding,
  * w16 = ws[m] * wq[m][k] rounded to `type` (GQ_F16 or GQ_BF16; the weights of the other
- * 16-bit products are rounded so, too).  dy: [N] rows of M elements of `type`, ldd >= M
+ * 16-bit products are rounded so, too): a binary16 weight above 65504 is infinite, one below
+ * 2^-14 has fewer bits, and against unrounded weights dX is off by 1.4 times what rounding dX
+ * alone costs.  dy: [N] rows of M elements of `type`, ldd >= M
  * elements apart (ldd unused when N is 1).  dx: [N][K] of `type`.  wsp: at least
  * gq_gemm_i8_backward_workspace_bytes(M, K, N, ldd) bytes, 16-byte aligned, contents on entry
  * ignored; not to be in use by another call while this one runs; it may be NULL where that is
@@ -615,7 +617,8 @@ typedef enum gq_act {
 /* The gate and up products of a feed-forward layer, the activation and the elementwise
  * product in one launch, from int8 activations:
  *   h[n][i] = round( act(g) * u ),  g = W_gate x, u = W_up x as gq_gemm_i8 forms them in
- *   binary32, the epilogue in binary32.
+ *   binary32, the epilogue in binary32 (for 16-bit results with the exponential instruction, off
+ *   by |g| 2^-24 and a few 2^-24 of it, and a sigmoid below 2^-126 is zero).
  * wq_gate, wq_up: I rows of H codes.  xq, xs: N rows of H codes.  h: [N][I] of h_type (any
  * gq_dtype).  Requires the limits of gq_gemm_i8 for M = I, K = H; I = 0 or N = 0 launches
  * nothing. */
